@@ -37,6 +37,30 @@ from ._binding import (  # noqa: F401
     workspace_views,
 )
 
+from ._modified import (  # noqa: F401,E402
+    AttentionMask,
+    ModifiedAttention,
+    attention_mask,
+    fa_bwd_mod,
+    fa_fwd_mod,
+    fa_mask_plan,
+    fa_mask_plan_size,
+)
+from .positions import (  # noqa: F401,E402
+    RotaryEmbedding,
+    fa_rotary,
+    rotary_backward,
+    rotary_embedding,
+    rotary_forward,
+    rotary_table,
+)
+from .paged import (  # noqa: F401,E402
+    fa_paged_append,
+    fa_paged_attention,
+    fa_paged_workspace_size,
+    paged_append,
+    paged_attention,
+)
 from .shard import head_ranges, shard_view, sharded_attention, sharded_attention_devices  # noqa: F401,E402
 
-__version__ = "2.0.0"
+__version__ = "2.1.0"

@@ -22,6 +22,8 @@ SYMBOLS = (
     "fa_bwd_dkdv", "fa_bwd_dq", "fa_status_string", "fa_device_status", "fa_version",
     "fa_bwd_noalloc", "fa_fwd_f16", "fa_bwd_f16", "fa_bwd_deterministic",
     "fa_bwd_deterministic_workspace_size", "fa_bwd_dkdvdq", "fa_bwd_dq_finish",
+    "fa_mask_plan_size", "fa_mask_plan", "fa_fwd_mod", "fa_bwd_mod", "fa_rotary", "fa_paged_append",
+    "fa_paged_workspace_size", "fa_paged_attention",
 )
 
 _lib = None
@@ -65,8 +67,20 @@ def load_library() -> ctypes.CDLL:
     lib.fa_version.argtypes = []
     for name in ("fa_fwd", "fa_fwd_f32", "fa_fwd_f16", "fa_bwd", "fa_bwd_f16", "fa_bwd_preprocess", "fa_bwd_dkdv",
                  "fa_bwd_dq", "fa_device_status", "fa_version", "fa_bwd_deterministic", "fa_bwd_dkdvdq",
-                 "fa_bwd_dq_finish"):
+                 "fa_bwd_dq_finish", "fa_mask_plan", "fa_fwd_mod", "fa_bwd_mod", "fa_rotary", "fa_paged_append",
+                 "fa_paged_attention"):
         getattr(lib, name).restype = i
+    ll = ctypes.c_longlong
+    lib.fa_mask_plan_size.argtypes = [i, i]
+    lib.fa_mask_plan_size.restype = sz
+    lib.fa_mask_plan.argtypes = [vp, sz, vp, vp, i, i, i, i, vp]
+    lib.fa_fwd_mod.argtypes = [vp] * 7 + [f] + [i] * 5 + [f, i, i, vp]
+    lib.fa_bwd_mod.argtypes = [vp] * 10 + [sz, vp, vp, f] + [i] * 5 + [f, i, i, vp]
+    lib.fa_rotary.argtypes = [vp] * 8 + [ll] + [i] * 10 + [vp]
+    lib.fa_paged_append.argtypes = [vp] * 13 + [i] * 12 + [vp]
+    lib.fa_paged_workspace_size.argtypes = [i] * 5
+    lib.fa_paged_workspace_size.restype = sz
+    lib.fa_paged_attention.argtypes = [vp] * 8 + [sz, vp, f] + [i] * 9 + [f, i, vp]
     _lib = lib
     return lib
 
@@ -262,10 +276,18 @@ def fa_version() -> int:
 
 
 # ----------------------------------------------------------------------------- convenience API
-def attention_forward(q, k, v, scale: float | None = None, causal: bool = False, stream=None):
-    """Returns (O, lse).  bf16 and fp16 inputs use the tensor-core path, float32 inputs the fp32 path."""
+def attention_forward(q, k, v, scale: float | None = None, causal: bool = False, stream=None, *, mask=None,
+                      softcap: float = 0.0, alibi_slopes=None):
+    """Returns (O, lse).  bf16 and fp16 inputs use the tensor-core path, float32 inputs the fp32 path.
+
+    bf16 and fp16 with head dims up to 128 also take, alone or together, k and v of fewer heads
+    (B,Hkv,N,D), an interval mask (attention_mask; instead of causal), softcap > 0 (scores become
+    softcap * tanh(score / softcap)) and alibi_slopes (float32 (H); slope * |i - j| is subtracted).
+    A row that sees no key has O = 0 and lse = -inf."""
     B, H, N, D = q.shape
     scale = default_scale(D) if scale is None else scale
+    if modified(q, k, mask, softcap, alibi_slopes):
+        return modified_forward(q, k, v, scale, causal, stream, mask, softcap, alibi_slopes)
     o = torch.empty_like(q)
     lse = torch.empty(B, H, N, device=q.device, dtype=torch.float32)
     if q.dtype == torch.float32:
@@ -278,11 +300,17 @@ def attention_forward(q, k, v, scale: float | None = None, causal: bool = False,
 
 
 def attention_backward(q, k, v, o, lse, do, scale: float | None = None, causal: bool = False, stream=None,
-                       workspace=None, deterministic: bool = False):
+                       workspace=None, deterministic: bool = False, *, mask=None, softcap: float = 0.0,
+                       alibi_slopes=None):
     """Returns (dQ, dK, dV) for bf16 or fp16 inputs (deterministic: bf16 only, the
-    bit-reproducible three-stage path)."""
+    bit-reproducible three-stage path).  mask, softcap, alibi_slopes and fewer key-value heads as
+    given to attention_forward (not with deterministic)."""
     B, H, N, D = q.shape
     scale = default_scale(D) if scale is None else scale
+    if modified(q, k, mask, softcap, alibi_slopes):
+        if deterministic:
+            raise ValueError("deterministic=True takes no mask, softcap, alibi_slopes or shared key-value heads")
+        return modified_backward(q, k, v, o, lse, do, scale, causal, stream, workspace, mask, softcap, alibi_slopes)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     size_fn = fa_bwd_deterministic_workspace_size if deterministic else fa_bwd_workspace_size
     if workspace is None:
@@ -312,9 +340,14 @@ class FlashAttention(torch.autograd.Function):
         return dq, dk, dv, None, None
 
 
-def flash_attention(q, k, v, scale: float | None = None, causal: bool = False):
-    """Differentiable exact attention on bf16 or fp16 (B,H,N,D) CUDA tensors."""
-    return FlashAttention.apply(q, k, v, default_scale(q.shape[-1]) if scale is None else scale, causal)
+def flash_attention(q, k, v, scale: float | None = None, causal: bool = False, *, mask=None, softcap: float = 0.0,
+                    alibi_slopes=None):
+    """Differentiable exact attention on bf16 or fp16 (B,H,N,D) CUDA tensors.  mask, softcap,
+    alibi_slopes and fewer key-value heads as in attention_forward; the slopes get no gradient."""
+    scale = default_scale(q.shape[-1]) if scale is None else scale
+    if modified(q, k, mask, softcap, alibi_slopes):
+        return ModifiedAttention.apply(q, k, v, scale, causal, mask, softcap, alibi_slopes)
+    return FlashAttention.apply(q, k, v, scale, causal)
 
 
 def attention_fwd_bwd_from_host(q_h, k_h, v_h, do_h, scale: float, causal: bool, dev_bufs=None, out=None,
@@ -430,3 +463,6 @@ class HostStepPipeline:
         """Waits until every queued step's results are in host memory."""
         for st in (self.s_h2d, self.s_comp, self.s_d2h):
             st.synchronize()
+
+
+from ._modified import ModifiedAttention, modified, modified_backward, modified_forward  # noqa: E402

@@ -82,7 +82,7 @@ int check_shape(int B, int H, int N, int D, bool sixteen_bit, bool with_256 = fa
 }
 
 // 3-D (D, N, B*H) bf16 (fp16 when f16) tensor map, box 64 x box_rows x 1, 128-byte swizzle.
-int make_tmap(CUtensorMap* map, const void* ptr, int BH, int N, int D, int box_rows, bool f16) {
+int make_tmap(CUtensorMap* map, const void* ptr, long long BH, long long N, long long D, int box_rows, bool f16) {
   auto enc = encode_fn();
   if (!enc) return FA_ERR_LAUNCH;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(BH)};
@@ -121,9 +121,23 @@ int heads_per_group(long long bytes_per_head, int BH) {
 
 }  // namespace
 
+namespace fa {
+int device_info(int** status, int* num_sms) {
+  DeviceState* ds = nullptr;
+  const int st = device_state(&ds);
+  if (st != FA_OK) return st;
+  *status = ds->status;
+  *num_sms = ds->num_sms;
+  return FA_OK;
+}
+int encode_tmap_3d(CUtensorMap* map, const void* ptr, long long d0, long long d1, long long d2, int box_rows, bool f16) {
+  return make_tmap(map, ptr, d2, d1, d0, box_rows, f16);
+}
+}  // namespace fa
+
 extern "C" {
 
-int fa_version(void) { return 20000; }
+int fa_version(void) { return 20100; }
 
 const char* fa_status_string(int status) {
   switch (status) {
@@ -139,6 +153,7 @@ const char* fa_status_string(int status) {
     case FA_ERR_CUDA: return "FA_ERR_CUDA: CUDA runtime error";
     case FA_ERR_ARG: return "FA_ERR_ARG: invalid argument";
     case FA_ERR_NOALLOC_CAPACITY: return "FA_ERR_NOALLOC_CAPACITY: problem exceeds the fa_bwd_noalloc scratch size";
+    case FA_ERR_INDEX: return "FA_ERR_INDEX: a page, position or length lies outside its table";
     case FA_ERR_DEBUG_CHECK: return "FA_ERR_DEBUG_CHECK: a device-side check of the debug build failed";
     default: return "unknown fa_status";
   }
@@ -455,6 +470,290 @@ int fa_bwd_deterministic(const void* q, const void* k, const void* v, const void
                          int B, int H, int N, int D, float scale, int causal, void* stream) {
   return bwd_det16(q, k, v, o, dO, lse, dq, dk, dv, workspace, workspace_bytes, B, H, N, D, scale, causal, stream,
                    false);
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------------------- score-modified attention
+namespace {
+
+// Rows of a mask plan: its builder keeps a batch element's run starts in shared memory.
+constexpr int kPlanMaxRows = 1 << 18;
+
+bool dtype_ok(int dtype) { return dtype == FA_BF16 || dtype == FA_F16; }
+
+// Checks shared by the score-modified forward and backward, and the kernels' view of the mods.
+int mods_args(const int* plan, const float* slopes, float softcap, int B, int H, int Hkv, int N, int D, float scale,
+              int causal, int dtype, fa::ScoreMods* m) {
+  int st = check_shape(B, H, N, D, true);
+  if (st != FA_OK) return st;
+  if (Hkv < 1 || H % Hkv != 0) return FA_ERR_SHAPE;
+  if (plan && N > kPlanMaxRows) return FA_ERR_SHAPE;
+  if ((plan && !aligned16(plan)) || (slopes && (reinterpret_cast<uintptr_t>(slopes) & 3u))) return FA_ERR_ALIGN;
+  if (!scale_ok(scale) || (causal != 0 && causal != 1) || (plan && causal) || !dtype_ok(dtype)) return FA_ERR_ARG;
+  if (!std::isfinite(softcap) || softcap < 0.f) return FA_ERR_ARG;
+  m->plan = plan;
+  m->slopes = slopes;
+  m->softcap = softcap;
+  m->H = H;
+  m->Hkv = Hkv;
+  m->causal = causal;
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t fa_mask_plan_size(int B, int N) {
+  if (B < 1 || N < 1 || N > kPlanMaxRows) return 0;
+  return fa::mask_plan_ints(B, N) * sizeof(int);
+}
+
+int fa_mask_plan(void* plan, size_t plan_bytes, const int* documents, const int* prefix, int B, int N, int causal,
+                 int window, void* stream) {
+  const size_t need = fa_mask_plan_size(B, N);
+  if (need == 0) return FA_ERR_SHAPE;
+  if (!plan || plan_bytes < need) return FA_ERR_WORKSPACE;
+  if (!aligned16(plan)) return FA_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(documents) & 3u) || (reinterpret_cast<uintptr_t>(prefix) & 3u)) return FA_ERR_ALIGN;
+  if ((causal != 0 && causal != 1) || window < 0) return FA_ERR_ARG;
+  if (prefix && (!causal || documents || window)) return FA_ERR_ARG;
+  int* status = nullptr;
+  int sms = 0;
+  const int st = fa::device_info(&status, &sms);
+  if (st != FA_OK) return st;
+  return launch_status(fa::launch_mask_plan(static_cast<int*>(plan), documents, prefix, B, N, causal, window,
+                                            static_cast<cudaStream_t>(stream)));
+}
+
+int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse, const void* plan, const float* slopes,
+               float softcap, int B, int H, int Hkv, int N, int D, float scale, int causal, int dtype, void* stream) {
+  if (!q || !k || !v || !o || !lse) return FA_ERR_NULL;
+  fa::ScoreMods m{};
+  int st = mods_args(static_cast<const int*>(plan), slopes, softcap, B, H, Hkv, N, D, scale, causal, dtype, &m);
+  if (st != FA_OK) return st;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse)) return FA_ERR_ALIGN;
+  DeviceState* ds = nullptr;
+  if ((st = device_state(&ds)) != FA_OK) return st;
+  const bool f16 = dtype == FA_F16;
+  fa::FwdLaunch a{};
+  if ((st = make_tmap(&a.tmQ, q, B * H, N, D, 128, f16)) != FA_OK) return st;
+  if ((st = make_tmap(&a.tmK, k, B * Hkv, N, D, 128, f16)) != FA_OK) return st;
+  if ((st = make_tmap(&a.tmV, v, B * Hkv, N, D, 128, f16)) != FA_OK) return st;
+  if ((st = make_tmap(&a.tmO, o, B * H, N, D, 32, f16)) != FA_OK) return st;
+  a.f16 = f16;
+  a.lse = lse;
+  a.BH = B * H;
+  a.N = N;
+  a.D = D;
+  a.scale = scale;
+  a.causal = causal;
+  a.status = ds->status;
+  a.num_sms = ds->num_sms;
+  a.hg = heads_per_group(4LL * N * D * Hkv / H, a.BH);
+  return launch_status(fa::launch_fwd_mod(a, m, static_cast<cudaStream_t>(stream)));
+}
+
+int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const void* dO, const float* lse, void* dq,
+               void* dk, void* dv, void* workspace, size_t workspace_bytes, const void* plan, const float* slopes,
+               float softcap, int B, int H, int Hkv, int N, int D, float scale, int causal, int dtype, void* stream) {
+  if (!q || !k || !v || !o || !dO || !lse || !dq || !dk || !dv) return FA_ERR_NULL;
+  fa::ScoreMods m{};
+  int st = mods_args(static_cast<const int*>(plan), slopes, softcap, B, H, Hkv, N, D, scale, causal, dtype, &m);
+  if (st != FA_OK) return st;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(dO) || !aligned16(o) || !aligned16(lse) ||
+      !aligned16(dq) || !aligned16(dk) || !aligned16(dv))
+    return FA_ERR_ALIGN;
+  const bool f16 = dtype == FA_F16;
+  fa::BwdLaunch a{};
+  if ((st = workspace_views(workspace, workspace_bytes, B, H, N, D, true, &a)) != FA_OK) return st;
+  DeviceState* ds = nullptr;
+  if ((st = device_state(&ds)) != FA_OK) return st;
+  if ((st = make_tmap(&a.tmQ, q, B * H, N, D, 128, f16)) != FA_OK) return st;
+  if ((st = make_tmap(&a.tmK, k, B * Hkv, N, D, 128, f16)) != FA_OK) return st;
+  if ((st = make_tmap(&a.tmV, v, B * Hkv, N, D, 128, f16)) != FA_OK) return st;
+  if ((st = make_tmap(&a.tmdO, dO, B * H, N, D, 128, f16)) != FA_OK) return st;
+  if ((st = make_tmap(&a.tmdK, dk, B * Hkv, N, D, 32, f16)) != FA_OK) return st;
+  if ((st = make_tmap(&a.tmdV, dv, B * Hkv, N, D, 32, f16)) != FA_OK) return st;
+  a.f16 = f16;
+  a.BH = B * H;
+  a.N = N;
+  a.D = D;
+  a.scale = scale;
+  a.status = ds->status;
+  a.num_sms = ds->num_sms;
+  // The CTAs of one key-value head share Q, dO and the dQ accumulator of its H / Hkv query heads.
+  a.hg = heads_per_group(static_cast<long long>(a.Npad) * (4LL * D + 4LL * a.DK) * (H / Hkv), B * Hkv);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if ((st = preprocess16(o, dO, lse, workspace, workspace_bytes, B, H, N, D, true, stream, f16)) != FA_OK) return st;
+  if ((st = launch_status(fa::launch_bwd_fused_mod(a, m, s))) != FA_OK) return st;
+  return dq_finish16(workspace, workspace_bytes, dq, B, H, N, D, scale, stream, f16);
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------------------- rotary positions, paged cache
+namespace {
+
+// Pages hold a power of two of 8 to 256 positions; returns its logarithm or -1.
+int page_shift(int page_size) {
+  for (int s = 3; s <= 8; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+bool int_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool strides_ok(const long long* s) { return s[0] % 8 == 0 && s[1] % 8 == 0 && s[2] % 8 == 0 && s[0] >= 0 && s[1] >= 0 && s[2] >= 0; }
+
+// Shape of a rotary or append call: head dims of the 16-bit paths, tokens within a 31-bit grid.
+int rotary_shape(int B, int H, int Hkv, int N, int D, int R, bool with_table, int table_rows) {
+  const int st = check_shape(B, H > 0 ? H : 1, N, D, true, true);
+  if (st != FA_OK) return st;
+  if (H < 0 || Hkv < 0 || H + Hkv < 1) return FA_ERR_SHAPE;
+  if (static_cast<long long>(B) * N > INT_MAX || static_cast<long long>(H) + 2LL * Hkv > 65535) return FA_ERR_SHAPE;
+  if (with_table ? (R < 2 || R > D || R % 2 != 0 || table_rows < 1) : R != 0) return FA_ERR_ARG;
+  return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_rotary(const void* q, const void* k, void* q_out, void* k_out, const float* table, const int* positions,
+              const long long* q_strides, const long long* k_strides, long long position_stride, int table_rows, int B,
+              int H, int Hkv, int N, int D, int R, int interleaved, int inverse, int dtype, void* stream) {
+  if (!table || (H > 0 && (!q || !q_out || !q_strides)) || (Hkv > 0 && (!k || !k_out || !k_strides))) return FA_ERR_NULL;
+  int st = rotary_shape(B, H, Hkv, N, D, R, true, table_rows);
+  if (st != FA_OK) return st;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || !aligned16(table) ||
+      !int_aligned(positions))
+    return FA_ERR_ALIGN;
+  if ((H > 0 && !strides_ok(q_strides)) || (Hkv > 0 && !strides_ok(k_strides))) return FA_ERR_ALIGN;
+  if ((interleaved & ~1) || (inverse & ~1) || !dtype_ok(dtype) || position_stride < 0) return FA_ERR_ARG;
+  fa::RotaryLaunch a{};
+  int sms = 0;
+  if ((st = fa::device_info(&a.status, &sms)) != FA_OK) return st;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_out = static_cast<uint16_t*>(k_out);
+  for (int i = 0; i < 3; ++i) {
+    a.q_stride[i] = H > 0 ? q_strides[i] : 0;
+    a.k_stride[i] = Hkv > 0 ? k_strides[i] : 0;
+  }
+  a.table = table;
+  a.positions = positions;
+  a.position_stride = position_stride;
+  a.B = B, a.H = H, a.Hkv = Hkv, a.N = N, a.D = D, a.R = R;
+  a.table_rows = table_rows;
+  a.interleaved = interleaved;
+  a.inverse = inverse;
+  a.f16 = dtype == FA_F16;
+  return launch_status(fa::launch_rotary(a, static_cast<cudaStream_t>(stream)));
+}
+
+int fa_paged_append(const void* k, const void* v, void* k_pages, void* v_pages, const void* q, void* q_out,
+                    const int* block_table, const int* seq_lens, const int* new_lens, const float* table,
+                    const long long* k_strides, const long long* v_strides, const long long* q_strides, int table_rows,
+                    int table_width, int num_pages, int page_size, int B, int H, int Hkv, int T, int D, int R,
+                    int interleaved, int dtype, void* stream) {
+  if (!k || !v || !k_pages || !v_pages || !block_table || !seq_lens || !k_strides || !v_strides) return FA_ERR_NULL;
+  if (H > 0 && (!q || !q_out || !q_strides)) return FA_ERR_NULL;
+  if (Hkv < 1) return FA_ERR_SHAPE;
+  int st = rotary_shape(B, H, Hkv, T, D, R, table != nullptr, table_rows);
+  if (st != FA_OK) return st;
+  const int shift = page_shift(page_size);
+  if (shift < 0 || table_width < 1 || num_pages < 1 || (static_cast<long long>(table_width) << shift) > INT_MAX) return FA_ERR_SHAPE;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(q) ||
+      !aligned16(q_out) || !aligned16(table) || !int_aligned(block_table) || !int_aligned(seq_lens) || !int_aligned(new_lens))
+    return FA_ERR_ALIGN;
+  if (!strides_ok(k_strides) || !strides_ok(v_strides) || (H > 0 && !strides_ok(q_strides))) return FA_ERR_ALIGN;
+  if ((interleaved & ~1) || !dtype_ok(dtype)) return FA_ERR_ARG;
+  fa::RotaryLaunch a{};
+  int sms = 0;
+  if ((st = fa::device_info(&a.status, &sms)) != FA_OK) return st;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_out = static_cast<uint16_t*>(k_pages);
+  a.v_out = static_cast<uint16_t*>(v_pages);
+  for (int i = 0; i < 3; ++i) {
+    a.q_stride[i] = H > 0 ? q_strides[i] : 0;
+    a.k_stride[i] = k_strides[i];
+    a.v_stride[i] = v_strides[i];
+  }
+  a.table = table;
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.new_lens = new_lens;
+  a.B = B, a.H = H, a.Hkv = Hkv, a.N = T, a.D = D, a.R = R;
+  a.table_rows = table_rows;
+  a.table_width = table_width;
+  a.num_pages = num_pages;
+  a.page_shift = shift;
+  a.interleaved = interleaved;
+  a.f16 = dtype == FA_F16;
+  a.paged = 1;
+  return launch_status(fa::launch_rotary(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"
+
+// Shape of a paged attention call.
+static int paged_shape(int B, int H, int Hkv, int T, int D) {
+  if (T < 1 || T > FA_PAGED_MAX_TOKENS) return FA_ERR_SHAPE;
+  const int st = check_shape(B, H, T, D, true, true);
+  if (st != FA_OK) return st;
+  if (B > FA_PAGED_MAX_BATCH || Hkv < 1 || H % Hkv != 0 || static_cast<long long>(B) * H * T > INT_MAX) return FA_ERR_SHAPE;
+  return FA_OK;
+}
+
+extern "C" {
+
+size_t fa_paged_workspace_size(int B, int H, int Hkv, int T, int D) {
+  if (paged_shape(B, H, Hkv, T, D) != FA_OK) return 0;
+  return fa::paged_workspace_bytes(B, H, Hkv, T, D, 0);
+}
+
+int fa_paged_attention(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                       const int* seq_lens, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                       const float* slopes, float softcap, int window, int table_width, int num_pages, int page_size,
+                       int B, int H, int Hkv, int T, int D, float scale, int dtype, void* stream) {
+  if (!q || !k_pages || !v_pages || !block_table || !seq_lens || !o || !lse) return FA_ERR_NULL;
+  int st = paged_shape(B, H, Hkv, T, D);
+  if (st != FA_OK) return st;
+  const int shift = page_shift(page_size);
+  if (shift < 0 || table_width < 1 || num_pages < 1 || (static_cast<long long>(table_width) << shift) > INT_MAX) return FA_ERR_SHAPE;
+  if ((static_cast<long long>(num_pages) * Hkv) << shift > INT_MAX) return FA_ERR_SHAPE;
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !int_aligned(lse) ||
+      !int_aligned(block_table) || !int_aligned(seq_lens) || !int_aligned(slopes))
+    return FA_ERR_ALIGN;
+  if (!scale_ok(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0 || !dtype_ok(dtype)) return FA_ERR_ARG;
+  if (!workspace || workspace_bytes < fa_paged_workspace_size(B, H, Hkv, T, D)) return FA_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return FA_ERR_ALIGN;
+  fa::PagedLaunch a{};
+  if ((st = fa::device_info(&a.status, &a.num_sms)) != FA_OK) return st;
+  a.q = static_cast<const uint16_t*>(q);
+  a.k_pages = static_cast<const uint16_t*>(k_pages);
+  a.v_pages = static_cast<const uint16_t*>(v_pages);
+  a.block_table = block_table;
+  a.seq_lens = seq_lens;
+  a.slopes = slopes;
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  a.workspace = workspace;
+  a.B = B, a.H = H, a.Hkv = Hkv, a.T = T, a.D = D;
+  a.num_pages = num_pages;
+  a.page_shift = shift;
+  a.table_width = table_width;
+  a.window = window;
+  a.f16 = dtype == FA_F16;
+  a.scale = scale;
+  a.softcap = softcap;
+  return launch_status(fa::launch_paged_attention(a, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -74,13 +74,19 @@ struct FusedSmem {
   static_assert(kBytes > 116 * 1024, "one CTA per SM (each CTA allocates all 512 TMEM columns)");
 };
 
-template <int D, bool CAUSAL, bool F16>
+// The score-modified instances (MOD, see the forward) walk, per key tile of one key-value head, the
+// query tiles that meet it in each of the H / Hkv query heads that share that head, one head after
+// the other: dK_j and dV_j stay in tensor memory over all of them.  With CAP the score gradient
+// carries the factor 1 - tanh^2 = 4 sigma (1 - sigma), folded into a second 16-bit copy of P
+// (`pw`) before dS is formed, so dS is rounded as often as without a cap.
+template <int D, bool CAUSAL, bool F16, bool MOD, bool CAP, bool ALIBI>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_fused_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmdO,
                      const __grid_constant__ CUtensorMap tmdK, const __grid_constant__ CUtensorMap tmdV,
                      const float* __restrict__ ws_nl, const float* __restrict__ ws_delta, float* __restrict__ ws_dq,
-                     int N, int Npad, int BH, int nkt, int hg, float scale, int* status) {
+                     int N, int Npad, int BH, int nkt, int hg, float scale, int* status,
+                     const __grid_constant__ ScoreMods mods) {
   using L = FusedSmem<D>;
   using T = Tile<D, 128>;
   extern __shared__ uint8_t smem[];   // alignment checked below, not assumed
@@ -96,10 +102,26 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // Work item: key tile kt of head bh (causal: tile 0, which meets every query tile, first).
   const WorkItem wi = grouped_order(static_cast<int>(blockIdx.x), BH, nkt, hg);
-  const int bh = wi.bh, kt = wi.tile;
+  const int bh = wi.bh, kt = wi.tile;     // MOD: bh is a key-value head
   const int kv0 = kt * 128;
-  const int it0 = CAUSAL ? kt : 0;        // first query tile
-  const int n = nkt - it0;                // query tiles visited (>= 1)
+  int it0 = CAUSAL ? kt : 0;              // first query tile
+  int nq = nkt - it0;                     // query tiles of one query head that meet this key tile
+  int n = nq;                             // query tiles visited (>= 1; MOD: >= 0, over all heads)
+  int batch = 0, qh0 = bh;                // first query head
+  if constexpr (MOD) {
+    const int group = mods.H / mods.Hkv;
+    batch = bh / mods.Hkv;
+    qh0 = batch * mods.H + (bh - batch * mods.Hkv) * group;
+    if (mods.plan != nullptr) {
+      const int4 tl = mask_plan_view(mods.plan, BH / mods.Hkv, N).tiles[batch * nkt + kt];
+      it0 = tl.z;
+      nq = tl.w - tl.z;
+    } else {
+      it0 = mods.causal ? kt : 0;
+      nq = nkt - it0;
+    }
+    n = nq * group;
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(bar(L::kBarKV), 1);
@@ -144,34 +166,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_3d(sb + L::kOffK + c * T::kBox, &tmK, bar(L::kBarKV), c * 64, kv0, bh);
         tma_load_3d(sb + L::kOffV + c * T::kBox, &tmV, bar(L::kBarKV), c * 64, kv0, bh);
       }
-      int nq = 0, no = 0;
+      int nql = 0, no = 0;
       bool ok = true;
+      int qt = it0, qh = qh0;             // query tile and head of step i
       for (int i = 0; i < n; ++i) {
         const int s = i % L::kStages;
         const uint32_t ph = ((i / L::kStages) & 1) ^ 1;
-        const int q0 = (it0 + i) * 128;
+        const int q0 = qt * 128, bhq = qh;
+        if (++qt == it0 + nq) {
+          qt = it0;
+          ++qh;
+        }
         if (!(ok = mbar_wait(bar(L::kBarQEmpty + s), ph, abort_flag))) break;
         const uint32_t qf = bar(L::kBarQFull + s);
-        const size_t srow = static_cast<size_t>(bh) * Npad + q0;      // padded rows: always in bounds
-        const bool stats_in = FA_BOUNDS(srow + 128 <= static_cast<size_t>(BH) * Npad, status);
+        const size_t srow = static_cast<size_t>(bhq) * Npad + q0;     // padded rows: always in bounds
+        const bool stats_in = FA_BOUNDS(srow + 128 <= static_cast<size_t>(MOD ? BH / mods.Hkv * mods.H : BH) * Npad, status);
         mbar_arrive_expect_tx(qf, T::kBytes + (stats_in ? L::kStatBytes : 0));
         for (int c = 0; c < T::kNBox; ++c)
-          tma_load_3d(sb + L::kOffQ + s * T::kBytes + c * T::kBox, &tmQ, qf, c * 64, q0, bh);
+          tma_load_3d(sb + L::kOffQ + s * T::kBytes + c * T::kBox, &tmQ, qf, c * 64, q0, bhq);
         if (stats_in) {
           bulk_load(sb + L::kOffStat + s * L::kStatBytes, ws_nl + srow, 128 * 4, qf);
           bulk_load(sb + L::kOffStat + s * L::kStatBytes + 128 * 4, ws_delta + srow, 128 * 4, qf);
         }
-        ++nq;
+        ++nql;
         if (!(ok = mbar_wait(bar(L::kBarOEmpty + s), ph, abort_flag))) break;
         const uint32_t of = bar(L::kBarOFull + s);
         mbar_arrive_expect_tx(of, T::kBytes);
         for (int c = 0; c < T::kNBox; ++c)
-          tma_load_3d(sb + L::kOffdO + s * T::kBytes + c * T::kBox, &tmdO, of, c * 64, q0, bh);
+          tma_load_3d(sb + L::kOffdO + s * T::kBytes + c * T::kBox, &tmdO, of, c * 64, q0, bhq);
         ++no;
       }
       if (!ok) raise_error(status, abort_flag, kStatusTimeout);
       mbar_wait_drain(bar(L::kBarKV), 0);
-      for (int i = max(0, nq - L::kStages); i < nq; ++i)
+      for (int i = max(0, nql - L::kStages); i < nql; ++i)
         mbar_wait_drain(bar(L::kBarQFull + i % L::kStages), (i / L::kStages) & 1);
       for (int i = max(0, no - L::kStages); i < no; ++i)
         mbar_wait_drain(bar(L::kBarOFull + i % L::kStages), (i / L::kStages) & 1);
@@ -219,15 +246,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                   g > 0 ? 1u : 0u);
         tc_commit(bar(L::kBarDQFull));
       };
-      bool ok = mbar_wait_spin(bar(L::kBarKV), 0, abort_flag) &&
-                mbar_wait_spin(bar(L::kBarQFull), 0, abort_flag) && mbar_wait_spin(bar(L::kBarOFull), 0, abort_flag);
-      if (ok) {
+      bool ok = mbar_wait_spin(bar(L::kBarKV), 0, abort_flag);
+      const bool any = !MOD || n > 0;
+      if (any) ok = ok && mbar_wait_spin(bar(L::kBarQFull), 0, abort_flag) && mbar_wait_spin(bar(L::kBarOFull), 0, abort_flag);
+      if (ok && any) {
         tc_fence_after();
         issue_st(0);
         issue_dpt(0);
         ok = mbar_wait_spin(bar(L::kBarP), 0, abort_flag);
       }
-      if (ok) {
+      if (ok && any) {
         tc_fence_after();
         issue_acc(kColDV, kColS, sdO(0), true);                                   // dV = P^T dO_0
         tc_commit(bar(L::kBarOEmpty));
@@ -281,11 +309,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool key_oob = key >= N;                       // padding rows of the last key tile
     const bool tail = __any_sync(0xffffffffu, key_oob);  // warp-uniform
     const float scale_log2 = scale * kLog2e;
-    const float2 sl2 = make_float2(scale_log2, scale_log2);
+    // CAP: 2 cap log2e (times sigma), -cap log2e, and -2 scale log2e / cap (sigma's exponent)
+    const float x_scale = CAP ? 2.f * mods.softcap * kLog2e : scale_log2;
+    const float cap_add = CAP ? -mods.softcap * kLog2e : 0.f;
+    const float sig_scale = CAP ? -2.f * scale_log2 / mods.softcap : 0.f;
+    const float2 sl2 = make_float2(x_scale, x_scale);
+    int pqt = it0, pqh = 0;                              // MOD: query tile and head (within the group) of p_tile's next step
+    int dqt = it0, dqh = 0;                              // and of drain's
     // Row r of the dS^T tile (box g/2 holds queries [64(g/2), 64(g/2)+64)); chunk c of a row sits at c ^ (r % 8).
     uint8_t* ds_row = smem + L::kOffDS + (g >> 1) * L::kDSBox + r * 128;
     const int sw = r & 7;
-    float* dq_head = ws_dq + static_cast<size_t>(bh) * Npad * D;
+    float* dq_head = ws_dq + static_cast<size_t>(qh0) * Npad * D;
+    uint32_t pw[CAP ? 16 : 1];                           // CAP: packed P^T (1 - tanh^2)
     uint32_t pk[16];                                     // packed P^T of the current tile
     // dQ of the previous query tile (this thread: query row r, D/4 columns), held in registers
     // from its drain out of tensor memory until its 16-byte reductions are issued, a few at a
@@ -297,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr int kReds = kCols / 4;                     // reductions per thread per tile: 8 or 4
     uint32_t held[kCols];
     float* held_acc = dq_head + 4 * r;
-    const float* const acc_end = ws_dq + static_cast<size_t>(BH) * Npad * D;   // end of the accumulator
+    const float* const acc_end = ws_dq + static_cast<size_t>(MOD ? BH / mods.Hkv * mods.H : BH) * Npad * D;   // end of the accumulator
     (void)acc_end;
     auto red_held = [&](int q) {
       float* a = held_acc + (kReds * g + q) * 512;
@@ -314,8 +349,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       FA_CONVERGED(status);                              // warp-collective TMEM loads follow
       tc_fence_after();
       const float4* st = reinterpret_cast<const float4*>(smem + L::kOffStat + s * L::kStatBytes) + 8 * g;
-      const int qc0 = (it0 + i) * 128 + 32 * g;          // query of this thread's column 0
-      const bool edge = tail || (CAUSAL && __any_sync(0xffffffffu, qc0 < key + 32));   // warp-uniform
+      const int qc0 = (MOD ? pqt : it0 + i) * 128 + 32 * g;   // query of this thread's column 0
+      bool edge = tail || (CAUSAL && __any_sync(0xffffffffu, qc0 < key + 32));   // warp-uniform
+      const int2* rows = nullptr;                        // MOD: the intervals of this thread's 32 queries
+      float slope2 = 0.f;
+      if constexpr (MOD) {
+        if (mods.plan != nullptr) {
+          const MaskPlan plan = mask_plan_view(mods.plan, BH / mods.Hkv, N);
+          rows = plan.rows + static_cast<size_t>(batch) * Npad + qc0;
+          const int2 all = plan.groups[(static_cast<size_t>(batch) * Npad + qc0) / 32];
+          edge = all.x > kv0 || all.y < kv0 + 128;
+        } else {
+          edge = tail || (mods.causal && qc0 + 1 < kv0 + 128);
+        }
+        if (ALIBI) slope2 = mods.slopes[qh0 - batch * mods.H + pqh] * kLog2e;
+        if (++pqt == it0 + nq) {
+          pqt = it0;
+          ++pqh;
+        }
+      }
       // two halves of 16 columns (one TMEM load each), to keep the held dQ values in registers
       auto p_phase = [&](auto masked) {
 #pragma unroll
@@ -331,13 +383,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int h = 0; h < 2; ++h) {
               const int c2 = 2 * c4 + h, c = 2 * c2, cl = c - 16 * hf;
               const float2 nlp = h ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y);
-              const float2 sv = make_float2(__uint_as_float(sr[cl]), __uint_as_float(sr[cl + 1]));
-              float2 p = exp2_pair(__ffma2_rn(sv, sl2, nlp), poly_pair(c2));
+              float2 sv = make_float2(__uint_as_float(sr[cl]), __uint_as_float(sr[cl + 1]));
+              float2 add = nlp;
+              if constexpr (CAP) {
+                sv.x = rcp_approx(1.f + ex2_approx(sv.x * sig_scale));
+                sv.y = rcp_approx(1.f + ex2_approx(sv.y * sig_scale));
+                add = __fadd2_rn(add, make_float2(cap_add, cap_add));
+              }
+              if constexpr (ALIBI) {
+                const float d0 = static_cast<float>(qc0 + c - key);
+                add.x = fmaf(-slope2, fabsf(d0), add.x);
+                add.y = fmaf(-slope2, fabsf(d0 + 1.f), add.y);
+              }
+              float2 p = exp2_pair(__ffma2_rn(sv, sl2, add), poly_pair(c2));
               if (decltype(masked)::value) {
-                if (key_oob || (CAUSAL && key > qc0 + c)) p.x = 0.f;
-                if (key_oob || (CAUSAL && key > qc0 + c + 1)) p.y = 0.f;
+                if constexpr (MOD) {
+                  int4 iv;                               // (lo, hi) of queries c and c + 1
+                  if (rows != nullptr) iv = *reinterpret_cast<const int4*>(rows + c);
+                  else iv = mods.causal ? make_int4(0, qc0 + c + 1, 0, qc0 + c + 2) : make_int4(0, N, 0, N);
+                  if (key < iv.x || key >= iv.y || key_oob) p.x = 0.f;
+                  if (key < iv.z || key >= iv.w || key_oob) p.y = 0.f;
+                } else {
+                  if (key_oob || (CAUSAL && key > qc0 + c)) p.x = 0.f;
+                  if (key_oob || (CAUSAL && key > qc0 + c + 1)) p.y = 0.f;
+                }
               }
               pk[c2] = pack16<F16>(p.x, p.y);
+              if constexpr (CAP) {
+                // 1 - tanh^2 = 4 sigma (1 - sigma)
+                const float2 w = __fmul2_rn(p, __fmul2_rn(__fmul2_rn(sv, make_float2(4.f, 4.f)),
+                                                          __ffma2_rn(sv, make_float2(-1.f, -1.f), make_float2(1.f, 1.f))));
+                pw[c2] = pack16<F16>(w.x, w.y);
+              }
             }
             if (reds && kReds == 8 && (c4 & 1)) red_held(4 + (c4 >> 1));         // reductions 4..7
             if (reds && kReds == 4 && (c4 & 3) == 3) red_held(2 + (c4 >> 2));    // reductions 2, 3
@@ -375,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c2 = 2 * c4 + h, c = 2 * c2;
             const float2 dlp = h ? make_float2(dl.z, dl.w) : make_float2(dl.x, dl.y);
             const float2 dpv = make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1]));
-            const uint32_t pp = pk[8 * hf + c2];
+            const uint32_t pp = CAP ? pw[(8 * hf + c2) & (CAP ? 15 : 0)] : pk[8 * hf + c2];
             const float2 ds = __fmul2_rn(make_float2(unpack16_lo<F16>(pp), unpack16_hi<F16>(pp)),
                                          __ffma2_rn(dlp, make_float2(-1.f, -1.f), dpv));
             dsk[c2] = pack16<F16>(ds.x, ds.y);
@@ -412,13 +489,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       reg_fence(held);
       tc_fence_before();
       mbar_arrive(bar(L::kBarDQEmpty));
-      held_acc = dq_head + static_cast<size_t>(it0 + i) * 128 * D + 4 * r;
+      if constexpr (MOD) {
+        held_acc = dq_head + (static_cast<size_t>(dqh) * Npad + static_cast<size_t>(dqt) * 128) * D + 4 * r;
+        if (++dqt == it0 + nq) {
+          dqt = it0;
+          ++dqh;
+        }
+      } else {
+        held_acc = dq_head + static_cast<size_t>(it0 + i) * 128 * D + 4 * r;
+      }
 #pragma unroll
       for (int q = 0; q < kReds / 2; ++q) red_held(q);
       return true;
     };
 
-    bool ok = p_tile(0, false);
+    bool ok = (MOD && n == 0) || p_tile(0, false);
     for (int i = 0; ok && i < n; ++i) {
       ok = ds_tile(i);
       if (ok && i + 1 < n) {
@@ -429,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (ok) ok = drain(i);                             // + first half of dQ_i's
     }
-    if (ok) {
+    if (ok && (!MOD || n > 0)) {
 #pragma unroll
       for (int q = kReds / 2; q < kReds; ++q) red_held(q);   // the last tile's second half
     }
@@ -446,8 +531,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (g < 2 * nbox) {
         const bool is_dv = g < nbox;
         const int box = is_dv ? g : g - nbox;
-        stage_box_16<D, F16>(tb + (is_dv ? kColDV : kColDK), box, is_dv ? 1.f : scale,
-                             smem + (is_dv ? L::kOffV : L::kOffK), r);
+        uint8_t* stage = smem + (is_dv ? L::kOffV : L::kOffK);
+        if (!MOD || n > 0) {
+          stage_box_16<D, F16>(tb + (is_dv ? kColDV : kColDK), box, is_dv ? 1.f : scale, stage, r);
+        } else {                                          // no query sees these keys
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(stage + box * T::kBox + r * 128 + 16 * c) = make_uint4(0u, 0u, 0u, 0u);
+        }
         store_warp_box<D>(is_dv ? &tmdV : &tmdK, sb + (is_dv ? L::kOffV : L::kOffK), box, wrow, kv0, bh, lane, N);
       }
     }
@@ -501,24 +592,39 @@ __global__ void __launch_bounds__(256) bwd_dq_finish_kernel(const float* __restr
   }
 }
 
-template <int D, bool CAUSAL, bool F16>
-cudaError_t fused_impl(const BwdLaunch& a, cudaStream_t stream) {
+template <int D, bool CAUSAL, bool F16, bool MOD, bool CAP, bool ALIBI>
+cudaError_t fused_impl(const BwdLaunch& a, const ScoreMods& m, cudaStream_t stream) {
   using L = FusedSmem<D>;
-  auto kern = bwd_fused_kernel<D, CAUSAL, F16>;
+  auto kern = bwd_fused_kernel<D, CAUSAL, F16, MOD, CAP, ALIBI>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   const int nkt = (a.N + 127) / 128;
-  kern<<<static_cast<unsigned>(nkt) * a.BH, kThreads, L::kBytes, stream>>>(
-      a.tmQ, a.tmK, a.tmV, a.tmdO, a.tmdK, a.tmdV, a.ws_nl, a.ws_delta, a.ws_dq, a.N, a.Npad, a.BH, nkt, a.hg,
-      a.scale, a.status);
+  const int BH = MOD ? a.BH / m.H * m.Hkv : a.BH;     // one CTA per key tile of a key-value head
+  kern<<<static_cast<unsigned>(nkt) * BH, kThreads, L::kBytes, stream>>>(
+      a.tmQ, a.tmK, a.tmV, a.tmdO, a.tmdK, a.tmdV, a.ws_nl, a.ws_delta, a.ws_dq, a.N, a.Npad, BH, nkt, a.hg,
+      a.scale, a.status, m);
   return cudaGetLastError();
 }
 
 template <bool F16>
 cudaError_t fused_typed(const BwdLaunch& a, cudaStream_t stream) {
   // Head dims 32 and 96 run the 64- and 128-column kernels on zero-filled tile columns.
-  if (a.DK == 64) return a.causal ? fused_impl<64, true, F16>(a, stream) : fused_impl<64, false, F16>(a, stream);
-  return a.causal ? fused_impl<128, true, F16>(a, stream) : fused_impl<128, false, F16>(a, stream);
+  const ScoreMods none{};
+  if (a.DK == 64)
+    return a.causal ? fused_impl<64, true, F16, false, false, false>(a, none, stream)
+                    : fused_impl<64, false, F16, false, false, false>(a, none, stream);
+  return a.causal ? fused_impl<128, true, F16, false, false, false>(a, none, stream)
+                  : fused_impl<128, false, F16, false, false, false>(a, none, stream);
+}
+
+template <int D, bool F16>
+cudaError_t fused_mod_typed(const BwdLaunch& a, const ScoreMods& m, cudaStream_t stream) {
+  const bool cap = m.softcap != 0.f, alibi = m.slopes != nullptr;
+  if (cap)
+    return alibi ? fused_impl<D, false, F16, true, true, true>(a, m, stream)
+                 : fused_impl<D, false, F16, true, true, false>(a, m, stream);
+  return alibi ? fused_impl<D, false, F16, true, false, true>(a, m, stream)
+               : fused_impl<D, false, F16, true, false, false>(a, m, stream);
 }
 
 template <int DK, bool F16>
@@ -535,6 +641,12 @@ cudaError_t finish_impl(const BwdLaunch& a, void* dq, cudaStream_t stream) {
 cudaError_t launch_bwd_fused(const BwdLaunch& a, cudaStream_t stream) {
   if (a.DK != 64 && a.DK != 128) return cudaErrorInvalidValue;
   return a.f16 ? fused_typed<true>(a, stream) : fused_typed<false>(a, stream);
+}
+
+cudaError_t launch_bwd_fused_mod(const BwdLaunch& a, const ScoreMods& m, cudaStream_t stream) {
+  if (a.DK == 64) return a.f16 ? fused_mod_typed<64, true>(a, m, stream) : fused_mod_typed<64, false>(a, m, stream);
+  if (a.DK == 128) return a.f16 ? fused_mod_typed<128, true>(a, m, stream) : fused_mod_typed<128, false>(a, m, stream);
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_bwd_dq_finish(const BwdLaunch& a, void* dq, cudaStream_t stream) {

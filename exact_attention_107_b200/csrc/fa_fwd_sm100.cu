@@ -50,6 +50,7 @@ constexpr float kRescaleThreshold = 8.0f;
 template <int D>
 __device__ __forceinline__ bool poly_pair(int) { return false; }
 constexpr float kLn2 = 0.69314718055994530942f;
+constexpr float kLog2e = 1.44269504088896340736f;
 
 template <int D>
 struct FwdSmem {
@@ -78,11 +79,21 @@ struct FwdSmem {
   static_assert(kBytes <= 232448, "shared memory budget");
 };
 
-template <int D, bool CAUSAL, bool F16>
+// The score-modified instances (MOD) run the same pipeline with, per batch element, query rows
+// that see an interval of keys each (a mask plan, or full / causal), key-value heads shared by
+// H / Hkv query heads, and optionally
+//   CAP    x = cap tanh(s / cap) for s = scale q.k.  tanh(z) = 2 sigma(2z) - 1, so the score
+//          registers are replaced by sigma = 1 / (1 + 2^(-c s)) and the softmax runs on
+//          2 cap log2e sigma, its constant -cap joining only lse.  sigma's error, about 2^-22, is
+//          an error of cap 2^-21 in x; the hardware tanh's 2^-11 would be one of cap / 2000.
+//   ALIBI  x -= slope_h |i - j|, in fp32 on the scores before the row maximum.
+// Rows that see nothing get O = 0 and lse = -inf.
+template <int D, bool CAUSAL, bool F16, bool MOD, bool CAP, bool ALIBI>
 __global__ void __launch_bounds__(kThreads, 1)
     fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
-                    float* __restrict__ lse, int N, int BH, int nqb, int hg, float scale_log2, int* status) {
+                    float* __restrict__ lse, int N, int BH, int nqb, int hg, float scale_log2, int* status,
+                    const __grid_constant__ ScoreMods mods) {
   using L = FwdSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -99,16 +110,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   {
     const WorkItem wi = grouped_order(static_cast<int>(blockIdx.x), BH, nqb, hg);
     bh = wi.bh;
-    qblk = CAUSAL ? nqb - 1 - wi.tile : wi.tile;
+    qblk = (CAUSAL || MOD) ? nqb - 1 - wi.tile : wi.tile;
   }
   const int nkv_all = (N + kBN - 1) / kBN;
-  int q0[2], nkv[2];
+  // Query tile t meets the key tiles j0 + [ka[t], ka[t] + nkv[t]); j0 is the first key tile that
+  // either meets, 0 without a mask plan.
+  int q0[2], ka[2] = {0, 0}, nkv[2], j0 = 0;
+  int kv_bh = bh, batch = 0;
+  if constexpr (MOD) {
+    batch = bh / mods.H;
+    kv_bh = batch * mods.Hkv + (bh - batch * mods.H) / (mods.H / mods.Hkv);
+  }
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     q0[t] = qblk * 2 * kBM + t * kBM;
-    nkv[t] = (q0[t] >= N) ? 0 : (CAUSAL ? min(nkv_all, q0[t] / kBN + 1) : nkv_all);
+    const bool causal = MOD ? mods.causal != 0 : CAUSAL;
+    nkv[t] = (q0[t] >= N) ? 0 : (causal ? min(nkv_all, q0[t] / kBN + 1) : nkv_all);
+    if constexpr (MOD) {
+      if (mods.plan != nullptr && q0[t] < N) {
+        const int4 tl = mask_plan_view(mods.plan, BH / mods.H, N).tiles[batch * nkv_all + q0[t] / kBM];
+        ka[t] = tl.x;
+        nkv[t] = tl.y - tl.x;
+      }
+    }
   }
-  const int nkv_max = max(nkv[0], nkv[1]);
+  int nkv_max = max(nkv[0], nkv[1]);
+  if constexpr (MOD) {
+    j0 = nkv[0] == 0 ? ka[1] : (nkv[1] == 0 ? ka[0] : min(ka[0], ka[1]));
+#pragma unroll
+    for (int t = 0; t < 2; ++t) ka[t] = nkv[t] == 0 ? 0 : ka[t] - j0;
+    nkv_max = max(ka[0] + nkv[0], ka[1] + nkv[1]);
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(bar(L::kBarQFull), 1);
@@ -161,12 +193,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = mbar_wait(bar(L::kBarKEmpty + s), ph ^ 1, abort_flag))) break;
         mbar_arrive_expect_tx(bar(L::kBarKFull + s), L::kTile);
         for (int c = 0; c < L::kNBox; ++c)
-          tma_load_3d(sb + L::kOffK + s * L::kTile + c * L::kBox, &tmK, bar(L::kBarKFull + s), c * 64, j * kBN, bh);
+          tma_load_3d(sb + L::kOffK + s * L::kTile + c * L::kBox, &tmK, bar(L::kBarKFull + s), c * 64, (j0 + j) * kBN, kv_bh);
         ++nk;
         if (!(ok = mbar_wait(bar(L::kBarVEmpty + s), ph ^ 1, abort_flag))) break;
         mbar_arrive_expect_tx(bar(L::kBarVFull + s), L::kTile);
         for (int c = 0; c < L::kNBox; ++c)
-          tma_load_3d(sb + L::kOffV + s * L::kTile + c * L::kBox, &tmV, bar(L::kBarVFull + s), c * 64, j * kBN, bh);
+          tma_load_3d(sb + L::kOffV + s * L::kTile + c * L::kBox, &tmV, bar(L::kBarVFull + s), c * 64, (j0 + j) * kBN, kv_bh);
         ++nv;
       }
       if (!ok) raise_error(status, abort_flag, kStatusTimeout);
@@ -198,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t vb = sb + L::kOffV + (j % L::kStages) * L::kTile;
         mma_ts_x4<8, 16, 24, 128, 256, 384>(tmem + 256 + t * D, tmem + t * 128 + 32 * h,
                                             sdesc_sw128(vb + h * 4 * 2048, L::kBox, 1024), kIdO,
-                                            (j > 0 || h > 0) ? 1u : 0u);
+                                            (j > ka[t] || h > 0) ? 1u : 0u);
       };
       bool ok = mbar_wait_spin(bar(L::kBarQFull), 0, abort_flag);
       if (ok && nkv_max > 0) {
@@ -206,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok) {
           tc_fence_after();
           for (int t = 0; t < 2; ++t)
-            if (nkv[t] > 0) issue_s(t, 0);
+            if (nkv[t] > 0 && ka[t] == 0) issue_s(t, 0);
           tc_commit(bar(L::kBarKEmpty));
         }
       }
@@ -216,17 +248,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         bool k_next = false;
         for (int t = 0; t < 2; ++t) {
-          if (j >= nkv[t]) continue;
-          // P_t arrives in two halves; the first half's products start while the
-          // softmax still computes the second.
-          if (!(ok = mbar_wait_spin(bar(L::kBarPFull + t), j & 1, abort_flag))) break;
-          tc_fence_after();
-          issue_pv(t, j, 0);
-          if (!(ok = mbar_wait_spin(bar(L::kBarPFull + 2 + t), j & 1, abort_flag))) break;
-          tc_fence_after();
-          issue_pv(t, j, 1);
-          if (j == nkv[t] - 1) tc_commit(bar(L::kBarOFull + t));
-          if (j + 1 < nkv[t]) {
+          if (j >= ka[t] + nkv[t]) continue;
+          if (!MOD || j >= ka[t]) {
+            // P_t arrives in two halves; the first half's products start while the
+            // softmax still computes the second.
+            const uint32_t ph = static_cast<uint32_t>(j - ka[t]) & 1u;
+            if (!(ok = mbar_wait_spin(bar(L::kBarPFull + t), ph, abort_flag))) break;
+            tc_fence_after();
+            issue_pv(t, j, 0);
+            if (!(ok = mbar_wait_spin(bar(L::kBarPFull + 2 + t), ph, abort_flag))) break;
+            tc_fence_after();
+            issue_pv(t, j, 1);
+            if (j == ka[t] + nkv[t] - 1) tc_commit(bar(L::kBarOFull + t));
+          }
+          if (j + 1 < ka[t] + nkv[t] && (!MOD || j + 1 >= ka[t])) {
             if (!k_next) {
               const int jn = j + 1;
               if (!(ok = mbar_wait_spin(bar(L::kBarKFull + jn % L::kStages), (jn / L::kStages) & 1, abort_flag)))
@@ -238,6 +273,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (!ok) break;
+        if constexpr (MOD) {
+          // Neither tile meets key tile j + 1 (a gap between their ranges): release it unread.
+          if (!k_next && j + 1 < nkv_max) {
+            const int jn = j + 1;
+            if (!(ok = mbar_wait_spin(bar(L::kBarKFull + jn % L::kStages), (jn / L::kStages) & 1, abort_flag))) break;
+            k_next = true;
+          }
+        }
         tc_commit(bar(L::kBarVEmpty + s));
         if (k_next) tc_commit(bar(L::kBarKEmpty + (j + 1) % L::kStages));
       }
@@ -256,6 +299,27 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tO = tmem + lane_off + 256 + t * D;
     const int qrow = q0[t] + r;
     float m = -CUDART_INF_F, l = 0.f;
+    // MOD: the keys [lo, hi) that this row sees (none for rows past N).
+    int lo = 0, hi = 0;
+    float slope2 = 0.f, sig_scale = 0.f, lse_add = 0.f;   // slope * log2e; -2 scale / cap * log2e; -cap
+    float softmax_scale = scale_log2;                     // multiplies the score registers in the exponent
+    if constexpr (MOD) {
+      if (qrow < N) {
+        hi = mods.causal ? qrow + 1 : N;
+        if (mods.plan != nullptr) {
+          const int2 iv = mask_plan_view(mods.plan, BH / mods.H, N).rows[static_cast<size_t>(batch) * nkv_all * kBN + qrow];
+          lo = iv.x;
+          hi = iv.y;
+        }
+      }
+      if (CAP) {
+        sig_scale = -2.f * scale_log2 / mods.softcap;
+        softmax_scale = 2.f * mods.softcap * kLog2e;
+        lse_add = -mods.softcap;
+      }
+      if (ALIBI) slope2 = mods.slopes[bh - batch * mods.H] * kLog2e;
+    }
+    const float x_scale = ALIBI ? 1.f : softmax_scale;    // ALIBI scales before the bias is subtracted
     bool ok = true;
     for (int j = 0; j < nkv[t]; ++j) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarSFull + t), j & 1, abort_flag));
@@ -272,9 +336,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       reg_fence(sr[1]);
       reg_fence(sr[2]);
       reg_fence(sr[3]);
-      const int kv0 = j * kBN;
+      const int kv0 = MOD ? (j0 + ka[t] + j) * kBN : j * kBN;
       const bool diag = CAUSAL && (kv0 + kBN - 1 > q0[t]);
-      if (diag || kv0 + kBN > N) {
+      if constexpr (CAP) {
+#pragma unroll
+        for (int c = 0; c < kBN; ++c)
+          sr[c >> 5][c & 31] = __float_as_uint(
+              rcp_approx(1.f + ex2_approx(__uint_as_float(sr[c >> 5][c & 31]) * sig_scale)));
+      }
+      if constexpr (ALIBI) {
+        // x - slope |i - j|: linear in the column where every key of the tile lies on one side of
+        // the warp's rows, element by element around the diagonal.
+        const int wrow0 = qrow - lane;
+        const float d0 = static_cast<float>(qrow - kv0);
+        if (kv0 + kBN - 1 <= wrow0 || kv0 >= wrow0 + 31) {
+          const float s2 = kv0 >= wrow0 + 31 ? -slope2 : slope2;
+          const float base = -s2 * d0;
+#pragma unroll
+          for (int c = 0; c < kBN; ++c)
+            sr[c >> 5][c & 31] = __float_as_uint(
+                fmaf(__uint_as_float(sr[c >> 5][c & 31]), softmax_scale, fmaf(s2, static_cast<float>(c), base)));
+        } else {
+#pragma unroll
+          for (int c = 0; c < kBN; ++c)
+            sr[c >> 5][c & 31] = __float_as_uint(fmaf(__uint_as_float(sr[c >> 5][c & 31]), softmax_scale,
+                                                      -slope2 * fabsf(d0 - static_cast<float>(c))));
+        }
+      }
+      if constexpr (MOD) {
+        if (!__all_sync(0xffffffffu, lo <= kv0 && hi >= kv0 + kBN)) {
+          const int first = lo - kv0;
+          const unsigned width = static_cast<unsigned>(hi - lo);          // keep first <= c < first + width
+#pragma unroll
+          for (int c = 0; c < kBN; ++c)
+            if (static_cast<unsigned>(c - first) >= width) sr[c >> 5][c & 31] = 0xff800000u;   // -inf
+        }
+      } else if (diag || kv0 + kBN > N) {
         const int lim = min(CAUSAL ? qrow - kv0 : kBN - 1, N - 1 - kv0);   // keep columns c <= lim
 #pragma unroll
         for (int c = 0; c < kBN; ++c)
@@ -285,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int c = 0; c < kBN; c += 2)
         mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(sr[c >> 5][c & 31]),
                                  __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
-      const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale_log2;
+      const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * x_scale;
       const float m_new = fmaxf(m, m_tile);
       const bool need = m_new > m + kRescaleThreshold;                     // always true at j == 0
       const float m_use = need ? m_new : m;
@@ -296,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // announced on its own barrier, so the P V products of the first half overlap the
       // exponentials of the second.
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      const float2 sl2 = make_float2(scale_log2, scale_log2), neg2 = make_float2(neg, neg);
+      const float2 sl2 = make_float2(x_scale, x_scale), neg2 = make_float2(neg, neg);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         // P of keys [64h, 64h+64) as packed pairs, stored 16 pairs at a time (nothing reads
@@ -347,20 +444,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && nkv[t] > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarOFull + t), 0, abort_flag));
     if (!ok) {
       raise_error(status, abort_flag, kStatusTimeout);
-    } else if (nkv[t] > 0) {
+    } else if (nkv[t] > 0 || (MOD && q0[t] < N)) {
       FA_CONVERGED(status);
       tc_fence_after();
       // Epilogue: O / l -> bf16 / fp16 into this warp's 32 rows of the (now idle) Q_t tile,
       // in the 128-byte-swizzled layout the O tensor map expects, then one TMA store
       // per warp (rows past N are clipped by the hardware).
-      const float inv_l = 1.f / l;
+      const float inv_l = (MOD && l == 0.f) ? 0.f : 1.f / l;      // a row that sees no key: O = 0
       uint8_t* stage = smem + L::kOffQ + t * L::kTile;
 #pragma unroll
       for (int cc = 0; cc < D / 32; ++cc) {
         uint32_t o[32];
-        tmem_ld32(tO + cc * 32, o);
-        tmem_ld_wait();
-        reg_fence(o);
+        if (!MOD || nkv[t] > 0) {
+          tmem_ld32(tO + cc * 32, o);
+          tmem_ld_wait();
+          reg_fence(o);
+        } else {                                                  // no product was ever added
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0u;
+        }
         const int box = cc >> 1;
 #pragma unroll
         for (int q4 = 0; q4 < 4; ++q4) {
@@ -383,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk_wait_read0();
       }
       if (qrow < N && FA_BOUNDS(static_cast<size_t>(bh) < static_cast<size_t>(BH), status))
-        lse[static_cast<size_t>(bh) * N + qrow] = m * kLn2 + logf(l);
+        lse[static_cast<size_t>(bh) * N + qrow] = m * kLn2 + logf(l) + (CAP ? lse_add : 0.f);
     }
   }
 
@@ -396,17 +498,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int D, bool CAUSAL, bool F16>
-cudaError_t launch_impl(const FwdLaunch& a, cudaStream_t stream) {
+template <int D, bool CAUSAL, bool F16, bool MOD, bool CAP, bool ALIBI>
+cudaError_t launch_impl(const FwdLaunch& a, const ScoreMods& m, cudaStream_t stream) {
   using L = FwdSmem<D>;
-  auto kern = fwd_kernel<D, CAUSAL, F16>;
+  auto kern = fwd_kernel<D, CAUSAL, F16, MOD, CAP, ALIBI>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   const int nqb = (a.N + 2 * kBM - 1) / (2 * kBM);
   const unsigned grid = static_cast<unsigned>(nqb) * static_cast<unsigned>(a.BH);
   const float scale_log2 = a.scale * 1.44269504088896340736f;
   kern<<<grid, kThreads, L::kBytes, stream>>>(a.tmQ, a.tmK, a.tmV, a.tmO, a.lse, a.N, a.BH, nqb, a.hg, scale_log2,
-                                               a.status);
+                                               a.status, m);
   return cudaGetLastError();
 }
 
@@ -416,14 +518,33 @@ cudaError_t launch_typed(const FwdLaunch& a, cudaStream_t stream) {
   // the caller's D, so the TMA fills the missing columns of every loaded tile with
   // zeros (which add nothing to Q K^T and give zero columns of P V) and clips them
   // from every store.
-  if (a.D <= 64) return a.causal ? launch_impl<64, true, F16>(a, stream) : launch_impl<64, false, F16>(a, stream);
-  return a.causal ? launch_impl<128, true, F16>(a, stream) : launch_impl<128, false, F16>(a, stream);
+  const ScoreMods none{};
+  if (a.D <= 64)
+    return a.causal ? launch_impl<64, true, F16, false, false, false>(a, none, stream)
+                    : launch_impl<64, false, F16, false, false, false>(a, none, stream);
+  return a.causal ? launch_impl<128, true, F16, false, false, false>(a, none, stream)
+                  : launch_impl<128, false, F16, false, false, false>(a, none, stream);
+}
+
+template <int D, bool F16>
+cudaError_t launch_mod_typed(const FwdLaunch& a, const ScoreMods& m, cudaStream_t stream) {
+  const bool cap = m.softcap != 0.f, alibi = m.slopes != nullptr;
+  if (cap)
+    return alibi ? launch_impl<D, false, F16, true, true, true>(a, m, stream)
+                 : launch_impl<D, false, F16, true, true, false>(a, m, stream);
+  return alibi ? launch_impl<D, false, F16, true, false, true>(a, m, stream)
+               : launch_impl<D, false, F16, true, false, false>(a, m, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_fwd_16(const FwdLaunch& a, cudaStream_t stream) {
   return a.f16 ? launch_typed<true>(a, stream) : launch_typed<false>(a, stream);
+}
+
+cudaError_t launch_fwd_mod(const FwdLaunch& a, const ScoreMods& m, cudaStream_t stream) {
+  if (a.D <= 64) return a.f16 ? launch_mod_typed<64, true>(a, m, stream) : launch_mod_typed<64, false>(a, m, stream);
+  return a.f16 ? launch_mod_typed<128, true>(a, m, stream) : launch_mod_typed<128, false>(a, m, stream);
 }
 
 }  // namespace fa

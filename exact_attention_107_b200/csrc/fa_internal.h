@@ -8,6 +8,7 @@ namespace fa {
 
 constexpr int kStatusLaunch = 6;   // FA_ERR_LAUNCH (a kernel found its launch unusable)
 constexpr int kStatusTimeout = 7;  // FA_ERR_TIMEOUT
+constexpr int kStatusIndex = 13;   // FA_ERR_INDEX (a page, position or length outside its table)
 
 // Order of the CTAs of a (head, tile) grid.  Heads are taken in groups of `hg` whose
 // data fits in L2 together; inside a group the order is tile-major (tile 0 of every
@@ -25,6 +26,79 @@ __host__ __device__ inline WorkItem grouped_order(int cta, int BH, int ntiles, i
   return {g * hg + local % gh, local / gh};
 }
 
+// What the score-modified paths add to a call (fa_mod.cu, and the MOD instances of the forward
+// and fused backward kernels).  All pointers are device pointers.
+struct ScoreMods {
+  const int* plan;      // key intervals and tile ranges (see MaskPlan), or null: full / causal by `causal`
+  const float* slopes;  // per query head, or null: no distance bias
+  float softcap;        // 0: none
+  int H, Hkv;           // query and key-value heads per batch element
+  int causal;           // without a plan: 1 = key j visible to query i iff j <= i
+};
+
+// Layout of a mask plan for B batch elements of N rows (int32, 16-byte aligned), Npad = N
+// rounded up to a multiple of 128, nt = Npad / 128:
+//   rows    [B][Npad]     int2  (lo, hi): row i sees the keys lo <= j < hi (padding rows: 0, 0)
+//   groups  [B][Npad/32]  int2  (largest lo, smallest hi) of 32 rows: keys in between are seen by all
+//   tiles   [B][nt]       int4  (first, end) key tile that query tile t meets, (first, end) query
+//                               tile that key tile t meets; first = end where there is none
+struct MaskPlan {
+  const int2* rows;
+  const int2* groups;
+  const int4* tiles;
+};
+__host__ __device__ inline size_t mask_plan_ints(size_t B, size_t N) {
+  const size_t npad = (N + 127) / 128 * 128;
+  return B * (2 * npad + 2 * (npad / 32) + 4 * (npad / 128));
+}
+__host__ __device__ inline MaskPlan mask_plan_view(const int* plan, int B, int N) {
+  const size_t npad = (static_cast<size_t>(N) + 127) / 128 * 128;
+  MaskPlan v;
+  v.rows = reinterpret_cast<const int2*>(plan);
+  v.groups = v.rows + B * npad;
+  v.tiles = reinterpret_cast<const int4*>(v.groups + B * (npad / 32));
+  return v;
+}
+// Builds a plan from optional document ids (B, N) and prefix lengths (B) (fa_mod.cu).
+cudaError_t launch_mask_plan(int* plan, const int* documents, const int* prefix, int B, int N, int causal, int window,
+                             cudaStream_t stream);
+
+// Shared by the C-ABI files: per-device status word and SM count of the current device, and
+// tensor-map encoding (fa_api.cu).  Both return an fa_status.
+int device_info(int** status, int* num_sms);
+int encode_tmap_3d(CUtensorMap* map, const void* ptr, long long d0, long long d1, long long d2, int box_rows, bool f16);
+
+// Rotary positions and cache append (fa_rotary.cu).  Strides are in elements: batch, head, token.
+struct RotaryLaunch {
+  const uint16_t *q, *k, *v;
+  uint16_t *q_out, *k_out, *v_out;   // paged: k_out / v_out are the page pools
+  long long q_stride[3], k_stride[3], v_stride[3];
+  const float* table;                // (table_rows, R): cos[R/2], sin[R/2]
+  const int* positions;              // rotary: (B or 1, N), or null: 0 .. N-1
+  long long position_stride;         // elements between batch elements (0: shared)
+  const int *block_table, *seq_lens, *new_lens;   // paged (new_lens may be null: N for all)
+  int B, H, Hkv, N, D, R, table_rows, table_width, num_pages, page_shift;
+  int interleaved, inverse, f16, paged;
+  int* status;
+};
+cudaError_t launch_rotary(const RotaryLaunch& a, cudaStream_t stream);
+
+// Attention of T new tokens a sequence over a paged cache (fa_paged.cu).
+struct PagedLaunch {
+  const uint16_t *q, *k_pages, *v_pages;   // q (B,H,T,D); pages (num_pages, Hkv, page, D)
+  const int *block_table, *seq_lens;       // (B, table_width), (B)
+  const float* slopes;                     // (H) or null
+  uint16_t* o;
+  float* lse;
+  void* workspace;
+  int B, H, Hkv, T, D, num_pages, page_shift, table_width, window, f16;
+  float scale, softcap;
+  int* status;
+  int num_sms;
+};
+size_t paged_workspace_bytes(int B, int H, int Hkv, int T, int D, int num_sms);
+cudaError_t launch_paged_attention(const PagedLaunch& a, cudaStream_t stream);
+
 // bf16 / fp16 forward (fa_fwd_sm100.cu).  Tensor maps are 3-D (D, N, B*H) of the
 // element type with 64 x 128 x 1 boxes (O: 64 x 32 x 1) and 128-byte swizzle.
 struct FwdLaunch {
@@ -39,6 +113,8 @@ struct FwdLaunch {
   int num_sms;
 };
 cudaError_t launch_fwd_16(const FwdLaunch& a, cudaStream_t stream);
+// Score-modified forward (head dims up to 128); a.BH counts query heads, tmK / tmV key-value heads.
+cudaError_t launch_fwd_mod(const FwdLaunch& a, const ScoreMods& m, cudaStream_t stream);
 // Head dimension 256 (fa_fwd_d256_sm100.cu): one query tile per CTA, same tensor maps.
 cudaError_t launch_fwd_d256(const FwdLaunch& a, cudaStream_t stream);
 
@@ -73,6 +149,8 @@ cudaError_t launch_bwd_dq(const BwdLaunch& a, cudaStream_t stream);
 // Fused backward (fa_bwd_fused_sm100.cu), DK in {64, 128}: dK, dV written, dQ added into
 // ws_dq (which the preprocess kernel zeroed); then dq_finish writes scale * ws_dq to dq.
 cudaError_t launch_bwd_fused(const BwdLaunch& a, cudaStream_t stream);
+// Score-modified fused backward; a.BH counts query heads, tmK / tmV / tmdK / tmdV key-value heads.
+cudaError_t launch_bwd_fused_mod(const BwdLaunch& a, const ScoreMods& m, cudaStream_t stream);
 cudaError_t launch_bwd_dq_finish(const BwdLaunch& a, void* dq, cudaStream_t stream);
 // Head dimension 256 (fa_bwd_d256_sm100.cu): two CTAs per tile, one per half of D.
 cudaError_t launch_bwd_dkdv_d256(const BwdLaunch& a, cudaStream_t stream);

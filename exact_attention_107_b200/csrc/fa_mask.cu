@@ -1,0 +1,194 @@
+// fa_mask.cu -- builds the mask plan of the score-modified attention: per query row the interval
+// of keys that it sees, and per 128-row tile what the kernels may skip (layout: MaskPlan).
+//
+// Every mask offered is an interval [lo_i, hi_i) per row i:
+//   documents   runs of equal ids: lo, hi = first row of i's run, one past its last; id < 0: nothing
+//   causal      hi = min(hi, i + 1)
+//   prefix      hi = max(i + 1, prefix) (causal, without documents)
+//   window w    lo = max(lo, i - w + 1), and without causal hi = min(hi, i + w)
+//
+// One CTA per batch element.  The rows' run starts become one bit each (a ballot per warp, ids read
+// once, coalesced); a scan over the N / 32 words gives each word the last start before it and the
+// first one after it, so a row finds its run with a bit scan in its own word.  Bound by latency,
+// not by its 4 bytes read and 8.6 written a row: 1024 threads of one SM walk all N rows.
+#include <climits>
+#include <cstdint>
+
+#include "fa_internal.h"
+
+namespace fa {
+namespace {
+
+constexpr int kThreads = 1024;
+
+// Inclusive scan over the CTA's threads with `op`; `buf` holds 32 ints.
+template <typename Op>
+__device__ __forceinline__ int block_scan(int x, int* buf, int identity, Op op) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, d);
+    if (lane >= d) x = op(y, x);
+  }
+  if (lane == 31) buf[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    int y = buf[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, y, d);
+      if (lane >= d) y = op(z, y);
+    }
+    buf[lane] = y;
+  }
+  __syncthreads();
+  const int before = warp > 0 ? buf[warp - 1] : identity;
+  __syncthreads();
+  return op(before, x);
+}
+
+__global__ void __launch_bounds__(kThreads) mask_plan_kernel(int* __restrict__ plan, const int* __restrict__ documents,
+                                                             const int* __restrict__ prefix, int N, int causal,
+                                                             int window) {
+  extern __shared__ int sh[];
+  const int b = blockIdx.x, B = gridDim.x;
+  const int nt = (N + 127) / 128, npad = nt * 128, nw = npad / 32;
+  int* tile_lo = sh;                 // [nt] smallest key seen by a row of the tile
+  int* tile_hi = tile_lo + nt;       // [nt] one past the largest
+  int* scan_buf = tile_hi + nt;      // [32]
+  unsigned* starts = reinterpret_cast<unsigned*>(scan_buf + 32);   // [nw] (documents only, as the next two)
+  int* last_before = reinterpret_cast<int*>(starts + nw);          // [nw] last run start in the words before
+  int* first_after = last_before + nw;                              // [nw] first run start in the words after
+  const MaskPlan v = mask_plan_view(plan, B, N);
+  int2* rows = const_cast<int2*>(v.rows) + static_cast<size_t>(b) * npad;
+  int2* groups = const_cast<int2*>(v.groups) + static_cast<size_t>(b) * (npad / 32);
+  int4* tiles = const_cast<int4*>(v.tiles) + static_cast<size_t>(b) * nt;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int* doc = documents != nullptr ? documents + static_cast<size_t>(b) * N : nullptr;
+
+  for (int t = threadIdx.x; t < nt; t += kThreads) {
+    tile_lo[t] = INT_MAX;
+    tile_hi[t] = 0;
+  }
+  if (doc != nullptr) {
+#pragma unroll 4
+    for (int w = warp; w < nw; w += kThreads / 32) {
+      const int i = w * 32 + lane;
+      const bool start = i < N && (i == 0 || doc[i] != doc[i - 1]);
+      const unsigned bits = __ballot_sync(0xffffffffu, start);
+      if (lane == 0) starts[w] = bits;
+    }
+    __syncthreads();
+    // each thread owns `per` consecutive words
+    const int per = (nw + kThreads - 1) / kThreads;
+    const int w0 = threadIdx.x * per, w1 = min(nw, w0 + per);
+    int last = -1, first = INT_MAX;
+    for (int w = w0; w < w1; ++w)
+      if (starts[w] != 0u) last = w * 32 + 31 - __clz(starts[w]);
+    for (int w = w1 - 1; w >= w0; --w)
+      if (starts[w] != 0u) first = w * 32 + __ffs(starts[w]) - 1;
+    // starts grow with the position: a running maximum from the left, a running minimum from the right
+    const int upto = block_scan(last, scan_buf, -1, [](int a, int c) { return max(a, c); });
+    int before = __shfl_up_sync(0xffffffffu, upto, 1);
+    if (lane == 31) scan_buf[warp] = upto;
+    __syncthreads();
+    if (lane == 0) before = warp > 0 ? scan_buf[warp - 1] : -1;
+    __syncthreads();
+    int carry = before;
+    for (int w = w0; w < w1; ++w) {
+      last_before[w] = carry;
+      if (starts[w] != 0u) carry = w * 32 + 31 - __clz(starts[w]);
+    }
+    // suffix minimum: warp-level shuffles down, then over the warps
+    int x = first;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_down_sync(0xffffffffu, x, d);
+      if (lane + d < 32) x = min(x, y);
+    }
+    if (lane == 0) scan_buf[warp] = x;
+    __syncthreads();
+    int after = __shfl_down_sync(0xffffffffu, x, 1);
+    if (lane == 31) after = INT_MAX;
+    for (int w = warp + 1; w < kThreads / 32; ++w) after = min(after, scan_buf[w]);
+    carry = after;
+    for (int w = w1 - 1; w >= w0; --w) {
+      first_after[w] = carry;
+      if (starts[w] != 0u) carry = w * 32 + __ffs(starts[w]) - 1;
+    }
+  }
+  __syncthreads();
+
+  const int pre = prefix != nullptr ? min(prefix[b], N) : 0;
+#pragma unroll 2
+  for (int w = warp; w < nw; w += kThreads / 32) {
+    const int i = w * 32 + lane;
+    int lo = 0, hi = N;
+    if (i >= N) {
+      hi = 0;
+    } else {
+      if (doc != nullptr) {
+        const unsigned bits = starts[w];
+        const unsigned upto = bits & (0xffffffffu >> (31 - lane));
+        const unsigned past = lane == 31 ? 0u : bits & (0xffffffffu << (lane + 1));
+        lo = upto != 0u ? w * 32 + 31 - __clz(upto) : last_before[w];
+        hi = past != 0u ? w * 32 + __ffs(past) - 1 : min(first_after[w], N);
+        if (doc[i] < 0) hi = lo;
+      }
+      if (causal) hi = min(hi, max(i + 1, pre));
+      if (window > 0) {
+        lo = max(lo, i - window + 1);
+        if (!causal && i < N - window) hi = min(hi, i + window);
+      }
+      if (hi <= lo) lo = hi = 0;
+    }
+    rows[i] = make_int2(lo, hi);
+    // rows past N constrain nothing
+    const int max_lo = __reduce_max_sync(0xffffffffu, i < N ? lo : 0);
+    const int min_hi = __reduce_min_sync(0xffffffffu, i < N ? hi : INT_MAX);
+    const int min_lo = __reduce_min_sync(0xffffffffu, hi > lo ? lo : INT_MAX);
+    const int max_hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+      groups[w] = make_int2(max_lo, min_hi);
+      atomicMin(&tile_lo[w >> 2], min_lo);
+      atomicMax(&tile_hi[w >> 2], max_hi);
+    }
+  }
+  __syncthreads();
+  // Key tile kt is met by the query tiles whose range holds it; every mask here makes them
+  // neighbours, up to tiles of rows that see nothing.
+  for (int t = threadIdx.x; t < nt; t += kThreads) {
+    int4 r = make_int4(0, 0, 0, 0);
+    if (tile_hi[t] > 0) {
+      r.x = tile_lo[t] / 128;
+      r.y = (tile_hi[t] + 127) / 128;
+    }
+    int q_first = INT_MAX, q_end = 0;
+    for (int q = 0; q < nt; ++q) {
+      if (tile_hi[q] > t * 128 && tile_lo[q] < t * 128 + 128) {
+        q_first = min(q_first, q);
+        q_end = q + 1;
+      }
+    }
+    if (q_end > 0) {
+      r.z = q_first;
+      r.w = q_end;
+    }
+    tiles[t] = r;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_mask_plan(int* plan, const int* documents, const int* prefix, int B, int N, int causal, int window,
+                             cudaStream_t stream) {
+  const size_t nt = (static_cast<size_t>(N) + 127) / 128;
+  const size_t bytes = (2 * nt + 32 + (documents != nullptr ? 3 * 4 * nt : 0)) * sizeof(int);
+  cudaError_t e = cudaFuncSetAttribute(mask_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(bytes));
+  if (e != cudaSuccess) return e;
+  mask_plan_kernel<<<B, kThreads, bytes, stream>>>(plan, documents, prefix, N, causal, window);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

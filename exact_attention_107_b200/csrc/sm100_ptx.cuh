@@ -310,6 +310,11 @@ __device__ __forceinline__ float ex2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 // Maximum that propagates NaN (max.NaN.f32): max(NaN, y) is NaN, max(-inf, y) is y.
 __device__ __forceinline__ float fmax_nan(float a, float b) {
   float r;

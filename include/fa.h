@@ -60,8 +60,12 @@ typedef enum {
   FA_ERR_CUDA = 9,             /* another CUDA runtime error                      */
   FA_ERR_ARG = 10,             /* another invalid argument (scale not finite ...) */
   FA_ERR_NOALLOC_CAPACITY = 11, /* problem too large for fa_bwd_noalloc's scratch  */
-  FA_ERR_DEBUG_CHECK = 12      /* a device-side check of the debug build failed   */
+  FA_ERR_DEBUG_CHECK = 12,     /* a device-side check of the debug build failed   */
+  FA_ERR_INDEX = 13            /* device data: a page, position or length outside its table */
 } fa_status;
+
+/* Element type of the entry points that take a `dtype`. */
+typedef enum { FA_BF16 = 0, FA_F16 = 1 } fa_dtype;
 
 /* Forward, bf16 in / bf16 out, fp32 accumulation (tcgen05 tensor cores).
  * Q/K/V tiles staged on chip and an online softmax with a running max and sum
@@ -219,6 +223,115 @@ int fa_bwd_dq(const void* q, const void* k, const void* v, const void* dO,
 int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, const void* dO,
                    const float* lse, void* dq, void* dk, void* dv,
                    int B, int H, int N, int D, float scale, int causal, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Score-modified attention: shared key-value heads, interval masks, capped scores
+ * and a distance bias, forward and backward, bf16 and fp16 (dtype), D in
+ * {32, 64, 96, 128}.  For query row i and key j of query head h:
+ *     s   = scale * q_i . k_j
+ *     x   = softcap * tanh(s / softcap)      (softcap > 0; 0: x = s)
+ *     x  -= slopes[h] * |i - j|              (slopes given: float32 (H))
+ *     P   = softmax of x over the keys that row i sees,  O = P V,
+ *     lse = ln(sum over them of exp(x)).
+ * A row that sees no key has O = 0 and lse = -inf, and gives no gradient.
+ * q, o, dO, dq are (B,H,N,D), lse (B,H,N); k, v, dk, dv are (B,Hkv,N,D) with H a
+ * multiple of Hkv: query head h reads key-value head h / (H / Hkv), and dk, dv sum
+ * over the query heads that share one.  Which keys a row sees is given by a plan
+ * (fa_mask_plan, with causal = 0 here), or without one (plan NULL) by `causal`.
+ * Values must be finite in every row, masked ones included: a masked key takes
+ * weight 0, and 0 times an infinity is not 0 (as in fa_fwd).
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of a mask plan for B batch elements of N rows; 0 if out of range (N up to
+ * 262144). */
+size_t fa_mask_plan_size(int B, int N);
+
+/* Builds the plan of an interval mask, to be used by any number of calls with the
+ * same B and N.  documents (int32 (B,N)) or NULL: rows i and j see each other only if
+ * every row from i to j carries the same id; a row with a negative id sees nothing
+ * and is not seen.  causal: key j allowed for query i iff j <= i; prefix (int32 (B))
+ * or NULL: or j < prefix[b] (causal only; not with documents or a window).
+ * window > 0: only i - j < window, and without causal also j - i < window. */
+int fa_mask_plan(void* plan, size_t plan_bytes, const int* documents, const int* prefix,
+                 int B, int N, int causal, int window, void* stream);
+
+/* Forward. */
+int fa_fwd_mod(const void* q, const void* k, const void* v, void* o, float* lse,
+               const void* plan, const float* slopes, float softcap,
+               int B, int H, int Hkv, int N, int D, float scale, int causal, int dtype, void* stream);
+
+/* Backward: o and lse from fa_fwd_mod with the same arguments; workspace of at least
+ * fa_bwd_workspace_size(B, H, N, D) bytes, contents ignored.  As in fa_bwd the fp32
+ * additions into dQ run in varying order (reproducible to rounding); dK and dV are
+ * deterministic. */
+int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const void* dO,
+               const float* lse, void* dq, void* dk, void* dv,
+               void* workspace, size_t workspace_bytes,
+               const void* plan, const float* slopes, float softcap,
+               int B, int H, int Hkv, int N, int D, float scale, int causal, int dtype, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions, and the paged key-value cache.  bf16 and fp16 (dtype), D in
+ * {32, 64, 96, 128, 256}.
+ * The table is float32 (table_rows, R): row p holds the R/2 cosines, then the R/2
+ * sines, of position p's angles.  The first R columns (even, 2 <= R <= D) turn in
+ * pairs (a, b) -> (a cos - b sin, b cos + a sin), pair i being columns (i, i + R/2),
+ * or (2i, 2i + 1) when interleaved; the rest is copied.
+ * Strides are in elements, for (batch, head, token), multiples of 8; the D columns of
+ * a row are contiguous.
+ * Index data (positions, pages, lengths) is read on the device: a value outside its
+ * table is never followed; the kernel records FA_ERR_INDEX in the device status word
+ * and leaves a row at such a position unturned, does not write such a page, and reads
+ * keys of such a page as absent.
+ * ------------------------------------------------------------------------- */
+
+/* q_out, k_out <- q, k with their rows turned; outputs contiguous (B,H,N,D) and
+ * (B,Hkv,N,D).  H = 0 or Hkv = 0 leaves that tensor out (its pointers may be NULL).
+ * positions: int32, row b at positions + b * position_stride, or NULL: 0 .. N-1.
+ * inverse = 1 turns by the negative angles: the gradient of inverse = 0. */
+int fa_rotary(const void* q, const void* k, void* q_out, void* k_out, const float* table,
+              const int* positions, const long long* q_strides, const long long* k_strides,
+              long long position_stride, int table_rows, int B, int H, int Hkv, int N, int D, int R,
+              int interleaved, int inverse, int dtype, void* stream);
+
+/* Writes the keys and values of new tokens into the pages of their sequences, turning
+ * the keys (and q into q_out) by their positions on the way.
+ *   k, v        (B,Hkv,T,D); q, q_out (B,H,T,D) or H = 0 without; q_out contiguous.
+ *   k_pages, v_pages (num_pages, Hkv, page_size, D) contiguous, page_size a power of
+ *               two from 8 to 256.
+ *   block_table int32 (B, table_width): page of positions [i page_size, (i+1) page_size).
+ *   seq_lens    int32 (B): length of each sequence WITH its new tokens.
+ *   new_lens    int32 (B), new tokens of each sequence (0 to T), or NULL: T.  Token t
+ *               of sequence b has position seq_lens[b] - new_lens[b] + t; rows
+ *               t >= new_lens[b] are not written, their q_out rows are zero.
+ *   table       or NULL with R = 0: nothing turns. */
+int fa_paged_append(const void* k, const void* v, void* k_pages, void* v_pages, const void* q, void* q_out,
+                    const int* block_table, const int* seq_lens, const int* new_lens, const float* table,
+                    const long long* k_strides, const long long* v_strides, const long long* q_strides,
+                    int table_rows, int table_width, int num_pages, int page_size,
+                    int B, int H, int Hkv, int T, int D, int R, int interleaved, int dtype, void* stream);
+
+/* Largest number of new tokens and of sequences of one fa_paged_attention call. */
+#define FA_PAGED_MAX_TOKENS 64
+#define FA_PAGED_MAX_BATCH 4096
+
+/* Bytes of device workspace fa_paged_attention needs; 0 for an unsupported shape. */
+size_t fa_paged_workspace_size(int B, int H, int Hkv, int T, int D);
+
+/* Attention of the last T tokens of each sequence (T = 1: one new token) over its
+ * paged cache, which already holds them (fa_paged_append).  q, o (B,H,T,D) contiguous,
+ * lse (B,H,T) float32.  Row t of sequence b has position p = seq_lens[b] - T + t and
+ * sees the keys j <= p, with window > 0 only those with p - j < window; x as in
+ * fa_fwd_mod with |i - j| = p - j.  A row with p < 0 (a sequence shorter than T, or
+ * empty) has O = 0 and lse = -inf.  Table entries past a sequence's last page and the
+ * slots behind its last position are never used, whatever they hold.
+ * Lengths beyond the table (table_width * page_size) are cut to it, with FA_ERR_INDEX.
+ * workspace: contents ignored and clobbered; calls that may overlap on the GPU need one
+ * each.  Results do not vary from run to run. */
+int fa_paged_attention(const void* q, const void* k_pages, const void* v_pages, const int* block_table,
+                       const int* seq_lens, void* o, float* lse, void* workspace, size_t workspace_bytes,
+                       const float* slopes, float softcap, int window, int table_width, int num_pages,
+                       int page_size, int B, int H, int Hkv, int T, int D, float scale, int dtype, void* stream);
 
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fa_status_string(int status);
