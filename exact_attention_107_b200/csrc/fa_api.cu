@@ -50,6 +50,9 @@ int device_state(DeviceState** out) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return FA_ERR_CUDA;
+  // A thread that has made no runtime call that needs it has no context yet (a backward pass runs on
+  // an autograd thread whose tensors may all come from cached blocks); tensor-map encoding needs one.
+  if (cudaSetDevice(dev) != cudaSuccess) return FA_ERR_CUDA;
   DeviceState& s = g_dev[dev];
   std::call_once(s.once, [&s, dev] {
     int major = 0, minor = 0;
@@ -715,7 +718,7 @@ extern "C" {
 
 size_t fa_paged_workspace_size(int B, int H, int Hkv, int T, int D) {
   if (paged_shape(B, H, Hkv, T, D) != FA_OK) return 0;
-  return fa::paged_workspace_bytes(B, H, Hkv, T, D, 0);
+  return fa::paged_workspace_bytes(H, Hkv, T, D);
 }
 
 int fa_paged_attention(const void* q, const void* k_pages, const void* v_pages, const int* block_table,

@@ -96,7 +96,7 @@ struct PagedLaunch {
   int* status;
   int num_sms;
 };
-size_t paged_workspace_bytes(int B, int H, int Hkv, int T, int D, int num_sms);
+size_t paged_workspace_bytes(int H, int Hkv, int T, int D);
 cudaError_t launch_paged_attention(const PagedLaunch& a, cudaStream_t stream);
 
 // bf16 / fp16 forward (fa_fwd_sm100.cu).  Tensor maps are 3-D (D, N, B*H) of the

@@ -1,9 +1,12 @@
 """Score-modified attention on the GPU (mask plan, forward, backward, autograd) against the 64-bit
 form, element by element."""
+import threading
+
 import pytest
 import torch
 
 import exact_attention_107_b200 as fa
+import exact_attention_107_b200._binding as base
 import operator_refs as ref
 
 pytestmark = pytest.mark.gpu
@@ -190,6 +193,37 @@ def test_autograd_matches_the_calls():
     assert ((leaves[0].grad - dq).abs() <= 2 ** -7 * dq.abs() + 1e-6).all()
     with pytest.raises(ValueError):
         fa.flash_attention(*leaves, alibi_slopes=slopes.clone().requires_grad_())
+
+
+def test_first_call_of_a_fresh_thread():
+    """A thread whose first CUDA work is one of the library's calls (as an autograd thread's may be)."""
+    B, H, N, D = 1, 2, 200, 64
+    q, k, v, do = (t.cuda() for t in inputs(B, H, H, N, D, "bf16", 8))
+    o, lse, dq, dk, dv, o2, lse2 = (torch.empty_like(t) for t in (q, q[..., 0].float(), q, k, v, q, q[..., 0].float()))
+    ws = torch.empty(fa.fa_bwd_workspace_size(B, H, N, D), device="cuda", dtype=torch.uint8)
+    stream = torch.cuda.current_stream().cuda_stream
+    failed = []
+
+    def run(call):
+        try:
+            call()
+        except Exception as e:                      # noqa: BLE001 - handed to the test's thread
+            failed.append(e)
+
+    code = lambda name, *args: base._raise(getattr(fa.load_library(), name)(*args), name)
+    p = base._p
+    for call in (lambda: code("fa_fwd_mod", p(q), p(k), p(v), p(o), p(lse), None, None, 30.0, B, H, H, N, D, 0.125, 1, 0, stream),
+                 lambda: code("fa_bwd_mod", p(q), p(k), p(v), p(o), p(do), p(lse), p(dq), p(dk), p(dv), p(ws),
+                              ws.numel(), None, None, 30.0, B, H, H, N, D, 0.125, 1, 0, stream),
+                 lambda: code("fa_fwd", p(q), p(k), p(v), p(o2), p(lse2), B, H, N, D, 0.125, 1, stream)):
+        t = threading.Thread(target=run, args=(call,))
+        t.start()
+        t.join()
+    assert not failed, failed
+    want = fa.attention_forward(q, k, v, 0.125, True, softcap=30.0)
+    grads = fa.attention_backward(q, k, v, *want, do, 0.125, True, softcap=30.0)
+    assert torch.equal(o, want[0]) and torch.equal(dk, grads[1]) and torch.equal(dv, grads[2])
+    assert torch.equal(o2, fa.attention_forward(q, k, v, 0.125, True)[0])
 
 
 def test_streams_and_graph():
