@@ -10,22 +10,28 @@ from torch.autograd.function import once_differentiable
 from . import _binding as base
 
 DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1}
+_device_now = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def stream_here(device, stream):
+    """The raw current stream where a call may launch as it is: no stream given and `device` current.
+    Otherwise None, and the call goes through launch_on."""
+    if stream is None and _device_now() == device.index:
+        return _raw_stream(device.index)
+    return None
 
 
 @contextlib.contextmanager
 def launch_on(device, stream):
     """Makes `device` and `stream` (None: the device's current stream; a torch.cuda.Stream or a raw
     cudaStream_t) current, so that what a call allocates belongs to the stream its kernels run on.
-    Yields a function that registers an output for use on the caller's own stream too."""
+    Yields the raw stream and a function that registers an output for use on the caller's own
+    stream too."""
     caller = torch.cuda.current_stream(device)
     if stream is None:
-        if torch.cuda.current_device() == device.index:
-            yield lambda t: t
-        else:
-            with torch.cuda.device(device):
-                yield lambda t: t
-        return
-    if not isinstance(stream, torch.cuda.Stream):
+        stream = caller
+    elif not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=device)
     if stream.device != device:
         raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
@@ -36,10 +42,25 @@ def launch_on(device, stream):
         return t
 
     with torch.cuda.device(device), torch.cuda.stream(stream):
-        yield keep
+        yield stream.cuda_stream, keep
+
+
+def no_keep(t):
+    return t
+
+
+def on(device, stream, call, *args):
+    """call(raw stream, keep, *args), launched on `device` and `stream`."""
+    raw = stream_here(device, stream)
+    if raw is not None:
+        return call(raw, no_keep, *args)
+    with launch_on(device, stream) as (raw, keep):
+        return call(raw, keep, *args)
 
 
 def check_on(t, name, dtype, shape, device) -> None:
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     base._check(t, name, dtype, shape)
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
@@ -50,9 +71,14 @@ def dtype_code(t, name) -> int:
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype not in DTYPE_CODES:
+    code = DTYPE_CODES.get(t.dtype)
+    if code is None:
         raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
-    return DTYPE_CODES[t.dtype]
+    return code
+
+
+def ptr(t):
+    return None if t is None else t.data_ptr()
 
 
 # ----------------------------------------------------------------------------- masks
@@ -76,9 +102,16 @@ def fa_mask_plan(plan, documents, prefix, B: int, N: int, causal: bool, window: 
         check_on(documents, "documents", torch.int32, (B, N), plan.device)
     if prefix is not None:
         check_on(prefix, "prefix", torch.int32, (B,), plan.device)
-    with launch_on(plan.device, stream):
-        base._raise(base.load_library().fa_mask_plan(pp, pn, base._p(documents), base._p(prefix), B, N, int(causal),
-                                                     int(window), base._stream(None)), "fa_mask_plan")
+    on(plan.device, stream, _mask_plan, pp, pn, documents, prefix, B, N, causal, window)
+
+
+def _mask_plan(raw, keep, pp, pn, documents, prefix, B, N, causal, window):
+    base._raise(base.load_library().fa_mask_plan(pp, pn, ptr(documents), ptr(prefix), B, N, int(causal), int(window),
+                                                 raw), "fa_mask_plan")
+
+
+def _new_plan(raw, keep, device, size):
+    return keep(torch.empty(size, device=device, dtype=torch.uint8))
 
 
 def attention_mask(B: int, N: int, *, documents=None, prefix=None, causal: bool = True, window: int = 0, device=None,
@@ -98,67 +131,80 @@ def attention_mask(B: int, N: int, *, documents=None, prefix=None, causal: bool 
     size = fa_mask_plan_size(B, N)
     if size == 0:
         raise base.FAError(2, "attention_mask")
-    with launch_on(device, stream) as keep:
-        plan = keep(torch.empty(size, device=device, dtype=torch.uint8))
-        fa_mask_plan(plan, documents, prefix, B, N, causal, window)
+    plan = on(device, stream, _new_plan, device, size)
+    fa_mask_plan(plan, documents, prefix, B, N, causal, window, stream)
     return AttentionMask(plan, B, N)
 
 
 # ----------------------------------------------------------------------------- C-ABI calls
 def _mod_args(q, k, v, mask, softcap, slopes, causal):
-    B, H, N, D = q.shape
+    """Checks what forward and backward share; returns the C call's tail up to the stream."""
     code = dtype_code(q, "q")
-    if k.dim() != 4:
-        raise ValueError(f"k must be (B,Hkv,N,D), got {tuple(k.shape)}")
+    if q.dim() != 4:
+        raise ValueError(f"q must be (B,H,N,D), got {tuple(q.shape)}")
+    B, H, N, D = q.shape
+    dev, dtype = q.device, q.dtype
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be (B,Hkv,N,D)")
     Hkv = k.shape[1]
-    base._check(q, "q", q.dtype, (B, H, N, D))
-    for name, t in (("k", k), ("v", v)):
-        check_on(t, name, q.dtype, (B, Hkv, N, D), q.device)
+    check_on(q, "q", dtype, (B, H, N, D), dev)
+    check_on(k, "k", dtype, (B, Hkv, N, D), dev)
+    check_on(v, "v", dtype, (B, Hkv, N, D), dev)
+    plan = None
     if mask is not None:
         if not isinstance(mask, AttentionMask):
             raise TypeError("mask must come from attention_mask")
-        if (mask.B, mask.N) != (B, N) or mask.plan.device != q.device:
-            raise ValueError(f"mask is for B={mask.B}, N={mask.N} on {mask.plan.device}; "
-                             f"q has B={B}, N={N} on {q.device}")
+        if mask.B != B or mask.N != N or mask.plan.device != dev:
+            raise ValueError(f"mask is for B={mask.B}, N={mask.N} on {mask.plan.device}; q has B={B}, N={N} on {dev}")
         if causal:
             raise ValueError("causal goes into attention_mask when a mask is given")
+        plan = mask.plan.data_ptr()
     if slopes is not None:
-        check_on(slopes, "alibi_slopes", torch.float32, (H,), q.device)
-    plan = None if mask is None else base._p(mask.plan)
-    return B, H, Hkv, N, D, code, plan
+        check_on(slopes, "alibi_slopes", torch.float32, (H,), dev)
+    return B, H, Hkv, N, D, code, (plan, ptr(slopes), float(softcap), B, H, Hkv, N, D)
 
 
 def fa_fwd_mod(q, k, v, o, lse, scale: float, causal: bool, mask=None, softcap: float = 0.0, alibi_slopes=None,
                stream=None) -> None:
     """O, lse <- score-modified attention; q, o (B,H,N,D), k, v (B,Hkv,N,D) bf16 or fp16, lse
     (B,H,N) float32."""
-    B, H, Hkv, N, D, code, plan = _mod_args(q, k, v, mask, softcap, alibi_slopes, causal)
+    B, H, _, N, D, code, mods = _mod_args(q, k, v, mask, softcap, alibi_slopes, causal)
     check_on(o, "o", q.dtype, (B, H, N, D), q.device)
     check_on(lse, "lse", torch.float32, (B, H, N), q.device)
-    with launch_on(q.device, stream):
-        base._raise(base.load_library().fa_fwd_mod(
-            base._p(q), base._p(k), base._p(v), base._p(o), base._p(lse), plan, base._p(alibi_slopes), float(softcap),
-            B, H, Hkv, N, D, float(scale), int(causal), code, base._stream(None)), "fa_fwd_mod")
+    on(q.device, stream, _fwd, q, k, v, o, lse, mods, scale, causal, code)
+
+
+def _fwd(raw, keep, q, k, v, o, lse, mods, scale, causal, code):
+    base._raise(base.load_library().fa_fwd_mod(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
+                                               *mods, float(scale), int(causal), code, raw), "fa_fwd_mod")
 
 
 def fa_bwd_mod(q, k, v, o, do, lse, dq, dk, dv, workspace, scale: float, causal: bool, mask=None, softcap: float = 0.0,
                alibi_slopes=None, stream=None) -> None:
     """dq, dk, dv <- gradients of fa_fwd_mod; workspace: uint8 CUDA tensor of
     fa_bwd_workspace_size(B, H, N, D) bytes."""
-    B, H, Hkv, N, D, code, plan = _mod_args(q, k, v, mask, softcap, alibi_slopes, causal)
-    for name, t in (("o", o), ("do", do), ("dq", dq)):
-        check_on(t, name, q.dtype, (B, H, N, D), q.device)
-    for name, t in (("dk", dk), ("dv", dv)):
-        check_on(t, name, q.dtype, (B, Hkv, N, D), q.device)
-    check_on(lse, "lse", torch.float32, (B, H, N), q.device)
-    wp, wn = base._ws(workspace)
+    B, H, Hkv, N, D, code, mods = _mod_args(q, k, v, mask, softcap, alibi_slopes, causal)
+    _check_grads(q, o, do, lse, B, H, N, D)
+    check_on(dq, "dq", q.dtype, (B, H, N, D), q.device)
+    check_on(dk, "dk", q.dtype, (B, Hkv, N, D), q.device)
+    check_on(dv, "dv", q.dtype, (B, Hkv, N, D), q.device)
+    base._ws(workspace)
     if workspace.device != q.device:
         raise ValueError(f"workspace must be on {q.device}")
-    with launch_on(q.device, stream):
-        base._raise(base.load_library().fa_bwd_mod(
-            base._p(q), base._p(k), base._p(v), base._p(o), base._p(do), base._p(lse), base._p(dq), base._p(dk),
-            base._p(dv), wp, wn, plan, base._p(alibi_slopes), float(softcap), B, H, Hkv, N, D, float(scale),
-            int(causal), code, base._stream(None)), "fa_bwd_mod")
+    on(q.device, stream, _bwd, q, k, v, o, do, lse, dq, dk, dv, workspace, mods, scale, causal, code)
+
+
+def _check_grads(q, o, do, lse, B, H, N, D):
+    check_on(o, "o", q.dtype, (B, H, N, D), q.device)
+    check_on(do, "do", q.dtype, (B, H, N, D), q.device)
+    check_on(lse, "lse", torch.float32, (B, H, N), q.device)
+
+
+def _bwd(raw, keep, q, k, v, o, do, lse, dq, dk, dv, workspace, mods, scale, causal, code):
+    base._raise(base.load_library().fa_bwd_mod(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+        dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), *mods,
+        float(scale), int(causal), code, raw), "fa_bwd_mod")
 
 
 # ----------------------------------------------------------------------------- convenience API
@@ -169,22 +215,33 @@ def modified(q, k, mask, softcap, alibi_slopes) -> bool:
 
 
 def modified_forward(q, k, v, scale, causal, stream, mask, softcap, alibi_slopes):
-    dtype_code(q, "q")
-    with launch_on(q.device, stream) as keep:
-        o = keep(torch.empty_like(q))
-        lse = keep(torch.empty(q.shape[:3], device=q.device, dtype=torch.float32))
-        fa_fwd_mod(q, k, v, o, lse, scale, causal, mask, softcap, alibi_slopes)
-    return o, lse
+    _, _, _, _, _, code, mods = _mod_args(q, k, v, mask, softcap, alibi_slopes, causal)
+
+    def call(raw, keep):
+        o, lse = keep(torch.empty_like(q)), keep(q.new_empty(q.shape[:3], dtype=torch.float32))
+        _fwd(raw, keep, q, k, v, o, lse, mods, scale, causal, code)
+        return o, lse
+
+    return on(q.device, stream, call)
 
 
 def modified_backward(q, k, v, o, lse, do, scale, causal, stream, workspace, mask, softcap, alibi_slopes):
-    dtype_code(q, "q")
-    with launch_on(q.device, stream) as keep:
-        dq, dk, dv = keep(torch.empty_like(q)), keep(torch.empty_like(k)), keep(torch.empty_like(v))
-        if workspace is None:
-            workspace = torch.empty(base.fa_bwd_workspace_size(*q.shape), device=q.device, dtype=torch.uint8)
-        fa_bwd_mod(q, k, v, o, do, lse, dq, dk, dv, workspace, scale, causal, mask, softcap, alibi_slopes)
-    return dq, dk, dv
+    B, H, Hkv, N, D, code, mods = _mod_args(q, k, v, mask, softcap, alibi_slopes, causal)
+    _check_grads(q, o, do, lse, B, H, N, D)
+    if workspace is not None:
+        base._ws(workspace)
+        if workspace.device != q.device:
+            raise ValueError(f"workspace must be on {q.device}")
+
+    def call(raw, keep):
+        grads = [keep(torch.empty_like(t)) for t in (q, k, v)]
+        ws = workspace
+        if ws is None:
+            ws = q.new_empty(base.fa_bwd_workspace_size(B, H, N, D), dtype=torch.uint8)
+        _bwd(raw, keep, q, k, v, o, do, lse, *grads, ws, mods, scale, causal, code)
+        return tuple(grads)
+
+    return on(q.device, stream, call)
 
 
 class ModifiedAttention(torch.autograd.Function):

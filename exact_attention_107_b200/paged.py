@@ -6,55 +6,70 @@ power of two from 8 to 256, an int32 block_table (B, width) that gives each sequ
 order, and int32 seq_lens (B), which count the new tokens of the current step."""
 from __future__ import annotations
 
+import functools
+
 import torch
 
 from . import _binding as base
-from ._modified import check_on, dtype_code, launch_on
+from ._modified import check_on, dtype_code, on, ptr
 from .positions import c_strides, check_strided, check_table, strides3
 
 
 def _check_cache(k_pages, v_pages, block_table, seq_lens, dtype, B, D, device):
     if not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
         raise ValueError("k_pages must be (num_pages, Hkv, page_size, D)")
-    num_pages, Hkv, page, _ = k_pages.shape
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        check_on(t, name, dtype, (num_pages, Hkv, page, D), device)
+    num_pages, Hkv, page, _ = shape = k_pages.shape
+    if shape[3] != D:
+        raise ValueError(f"k_pages must have {D} columns, got {tuple(shape)}")
+    check_on(k_pages, "k_pages", dtype, shape, device)
+    check_on(v_pages, "v_pages", dtype, shape, device)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be (B, pages per sequence)")
-    check_on(block_table, "block_table", torch.int32, (B, block_table.shape[1]), device)
+    width = block_table.shape[1]
+    check_on(block_table, "block_table", torch.int32, (B, width), device)
     check_on(seq_lens, "seq_lens", torch.int32, (B,), device)
-    return num_pages, Hkv, page, block_table.shape[1]
+    return num_pages, Hkv, page, width
+
+
+def _append_args(k, v, k_pages, v_pages, q, block_table, seq_lens, new_lens, table):
+    code = dtype_code(k, "k")
+    if k.dim() != 4:
+        raise ValueError(f"k must be (B,Hkv,T,D), got {tuple(k.shape)}")
+    B, Hkv, T, D = k.shape
+    dev, dtype = k.device, k.dtype
+    check_strided(v, "v", dtype, (B, Hkv, T, D), dev)
+    num_pages, heads, page, width = _check_cache(k_pages, v_pages, block_table, seq_lens, dtype, B, D, dev)
+    if heads != Hkv:
+        raise ValueError(f"k has {Hkv} heads, the pages {heads}")
+    H, qs = 0, None
+    if q is not None:
+        H = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 4 else 0
+        check_strided(q, "q", dtype, (B, H, T, D), dev)
+        qs = c_strides(strides3(q, "q"))
+    if new_lens is not None:
+        check_on(new_lens, "new_lens", torch.int32, (B,), dev)
+    R = rows = 0
+    if table is not None:
+        R, rows = check_table(table, D, dev), table.shape[0]
+    return (B, H, T, D), (c_strides(strides3(k, "k")), c_strides(strides3(v, "v")), qs, rows, width, num_pages, page,
+                          B, H, Hkv, T, D, R), code
+
+
+def _append(raw, keep, k, v, k_pages, v_pages, q, q_out, block_table, seq_lens, new_lens, table, args, interleaved, code):
+    base._raise(base.load_library().fa_paged_append(
+        k.data_ptr(), v.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), ptr(q), ptr(q_out), block_table.data_ptr(),
+        seq_lens.data_ptr(), ptr(new_lens), ptr(table), *args, int(interleaved), code, raw), "fa_paged_append")
 
 
 def fa_paged_append(k, v, k_pages, v_pages, q, q_out, block_table, seq_lens, new_lens=None, table=None,
                     interleaved: bool = False, stream=None) -> None:
     """The pages <- k (turned when a table is given), v; q_out <- q turned (q None: left out).
     Arguments as paged_append; q_out contiguous."""
-    code = dtype_code(k, "k")
-    if k.dim() != 4:
-        raise ValueError(f"k must be (B,Hkv,T,D), got {tuple(k.shape)}")
-    B, Hkv, T, D = k.shape
-    dev = k.device
-    check_strided(v, "v", k.dtype, (B, Hkv, T, D), dev)
-    num_pages, heads, page, width = _check_cache(k_pages, v_pages, block_table, seq_lens, k.dtype, B, D, dev)
-    if heads != Hkv:
-        raise ValueError(f"k has {Hkv} heads, the pages {heads}")
-    H, qs = 0, None
+    shape, args, code = _append_args(k, v, k_pages, v_pages, q, block_table, seq_lens, new_lens, table)
     if q is not None:
-        H = q.shape[1] if q.dim() == 4 else 0
-        check_strided(q, "q", k.dtype, (B, H, T, D), dev)
-        check_on(q_out, "q_out", k.dtype, (B, H, T, D), dev)
-        qs = c_strides(strides3(q, "q"))
-    if new_lens is not None:
-        check_on(new_lens, "new_lens", torch.int32, (B,), dev)
-    R = 0 if table is None else check_table(table, D, dev)
-    with launch_on(dev, stream):
-        base._raise(base.load_library().fa_paged_append(
-            base._p(k), base._p(v), base._p(k_pages), base._p(v_pages), base._p(q),
-            base._p(q_out if q is not None else None), base._p(block_table), base._p(seq_lens), base._p(new_lens),
-            base._p(table), c_strides(strides3(k, "k")), c_strides(strides3(v, "v")), qs,
-            0 if table is None else table.shape[0], width, num_pages, page, B, H, Hkv, T, D, R, int(interleaved), code,
-            base._stream(None)), "fa_paged_append")
+        check_on(q_out, "q_out", k.dtype, shape, k.device)
+    on(k.device, stream, _append, k, v, k_pages, v_pages, q, q_out if q is not None else None, block_table, seq_lens,
+       new_lens, table, args, interleaved, code)
 
 
 def paged_append(k, v, k_pages, v_pages, block_table, seq_lens, *, new_lens=None, q=None, table=None,
@@ -69,40 +84,59 @@ def paged_append(k, v, k_pages, v_pages, block_table, seq_lens, *, new_lens=None
     table is not written and sets the device status (fa_device_status) to FA_ERR_INDEX."""
     if table is None and q is not None:
         raise ValueError("q is turned on the way and needs a table")
-    dtype_code(k, "k")
-    with launch_on(k.device, stream) as keep:
-        q_out = None if q is None else keep(torch.empty(q.shape, device=q.device, dtype=q.dtype))
-        fa_paged_append(k, v, k_pages, v_pages, q, q_out, block_table, seq_lens, new_lens, table, interleaved)
-    return q_out
+    shape, args, code = _append_args(k, v, k_pages, v_pages, q, block_table, seq_lens, new_lens, table)
+
+    def call(raw, keep):
+        q_out = None if q is None else keep(q.new_empty(shape))
+        _append(raw, keep, k, v, k_pages, v_pages, q, q_out, block_table, seq_lens, new_lens, table, args, interleaved,
+                code)
+        return q_out
+
+    return on(k.device, stream, call)
 
 
+@functools.lru_cache(maxsize=256)
 def fa_paged_workspace_size(B: int, H: int, Hkv: int, T: int, D: int) -> int:
     return int(base.load_library().fa_paged_workspace_size(B, H, Hkv, T, D))
+
+
+def _decode_args(q, k_pages, v_pages, block_table, seq_lens, alibi_slopes):
+    code = dtype_code(q, "q")
+    if q.dim() != 4:
+        raise ValueError(f"q must be (B,H,T,D), got {tuple(q.shape)}")
+    B, H, T, D = q.shape
+    dev = q.device
+    check_on(q, "q", q.dtype, q.shape, dev)
+    num_pages, Hkv, page, width = _check_cache(k_pages, v_pages, block_table, seq_lens, q.dtype, B, D, dev)
+    if alibi_slopes is not None:
+        check_on(alibi_slopes, "alibi_slopes", torch.float32, (H,), dev)
+    return (width, num_pages, page, B, H, Hkv, T, D), code
+
+
+def _decode(raw, keep, q, k_pages, v_pages, block_table, seq_lens, o, lse, workspace, alibi_slopes, softcap, window,
+            args, scale, code):
+    base._raise(base.load_library().fa_paged_attention(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(),
+        o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        ptr(alibi_slopes), float(softcap), int(window), *args, float(scale), code, raw), "fa_paged_attention")
+
+
+def _check_workspace(workspace, dev):
+    base._ws(workspace)
+    if workspace.device != dev:
+        raise ValueError(f"workspace must be on {dev}")
 
 
 def fa_paged_attention(q, k_pages, v_pages, block_table, seq_lens, o, lse, workspace, scale: float,
                        softcap: float = 0.0, alibi_slopes=None, window: int = 0, stream=None) -> None:
     """o, lse <- paged_attention; o (B,H,T,D), lse (B,H,T) float32, workspace of
     fa_paged_workspace_size bytes (one for each call that may overlap)."""
-    code = dtype_code(q, "q")
-    if q.dim() != 4:
-        raise ValueError(f"q must be (B,H,T,D), got {tuple(q.shape)}")
-    B, H, T, D = q.shape
-    dev = q.device
-    base._check(q, "q", q.dtype, (B, H, T, D))
-    num_pages, Hkv, page, width = _check_cache(k_pages, v_pages, block_table, seq_lens, q.dtype, B, D, dev)
-    check_on(o, "o", q.dtype, (B, H, T, D), dev)
-    check_on(lse, "lse", torch.float32, (B, H, T), dev)
-    if alibi_slopes is not None:
-        check_on(alibi_slopes, "alibi_slopes", torch.float32, (H,), dev)
-    wp, wn = base._ws(workspace)
-    if workspace.device != dev:
-        raise ValueError(f"workspace must be on {dev}")
-    with launch_on(dev, stream):
-        base._raise(base.load_library().fa_paged_attention(
-            base._p(q), base._p(k_pages), base._p(v_pages), base._p(block_table), base._p(seq_lens), base._p(o),
-            base._p(lse), wp, wn, base._p(alibi_slopes), float(softcap), int(window), width, num_pages, page,
-            B, H, Hkv, T, D, float(scale), code, base._stream(None)), "fa_paged_attention")
+    args, code = _decode_args(q, k_pages, v_pages, block_table, seq_lens, alibi_slopes)
+    check_on(o, "o", q.dtype, q.shape, q.device)
+    check_on(lse, "lse", torch.float32, q.shape[:3], q.device)
+    _check_workspace(workspace, q.device)
+    on(q.device, stream, _decode, q, k_pages, v_pages, block_table, seq_lens, o, lse, workspace, alibi_slopes, softcap,
+       window, args, scale, code)
 
 
 def paged_attention(q, k_pages, v_pages, block_table, seq_lens, scale: float | None = None, *, softcap: float = 0.0,
@@ -113,21 +147,24 @@ def paged_attention(q, k_pages, v_pages, block_table, seq_lens, scale: float | N
     q (B,H,T,D), H a multiple of the pages' Hkv.  Row t of sequence b has position p =
     seq_lens[b] - T + t and sees keys j <= p, with window > 0 those with p - j < window; a row with
     p < 0 has O = 0 and lse = -inf.  softcap and alibi_slopes as in attention_forward, so that a
-    model trained there is served here.  Table entries past a sequence's last page are not read; a
-    page outside the pool counts as absent and sets the device status (fa_device_status) to
-    FA_ERR_INDEX.  workspace: for callers that keep one, of fa_paged_workspace_size bytes; calls
-    that may overlap on the GPU (other streams, captured graphs) must not share it."""
-    dtype_code(q, "q")
-    if q.dim() != 4 or not isinstance(k_pages, torch.Tensor) or k_pages.dim() != 4:
-        raise ValueError("q must be (B,H,T,D) and k_pages (num_pages, Hkv, page_size, D)")
-    B, H, T, D = q.shape
-    scale = base.default_scale(D) if scale is None else scale
-    with launch_on(q.device, stream) as keep:
-        o = keep(torch.empty(q.shape, device=q.device, dtype=q.dtype))
-        lse = keep(torch.empty(B, H, T, device=q.device, dtype=torch.float32))
-        if workspace is None:
-            workspace = torch.empty(max(16, fa_paged_workspace_size(B, H, k_pages.shape[1], T, D)), device=q.device,
-                                    dtype=torch.uint8)
-        fa_paged_attention(q, k_pages, v_pages, block_table, seq_lens, o, lse, workspace, scale, softcap,
-                           alibi_slopes, window)
-    return o, lse
+    model trained there is served here.  Table entries past a sequence's last page, or wholly before
+    every row's window, are not read; a page outside the pool counts as absent and sets the device
+    status (fa_device_status) to FA_ERR_INDEX.  workspace: for callers that keep one, of
+    fa_paged_workspace_size bytes; calls that may overlap on the GPU (other streams, captured
+    graphs) must not share it."""
+    args, code = _decode_args(q, k_pages, v_pages, block_table, seq_lens, alibi_slopes)
+    if scale is None:
+        scale = base.default_scale(q.shape[3])
+    if workspace is not None:
+        _check_workspace(workspace, q.device)
+
+    def call(raw, keep):
+        o, lse = keep(torch.empty_like(q)), keep(q.new_empty(q.shape[:3], dtype=torch.float32))
+        ws = workspace
+        if ws is None:
+            ws = q.new_empty(max(16, fa_paged_workspace_size(*args[3:])), dtype=torch.uint8)
+        _decode(raw, keep, q, k_pages, v_pages, block_table, seq_lens, o, lse, ws, alibi_slopes, softcap, window, args,
+                scale, code)
+        return o, lse
+
+    return on(q.device, stream, call)

@@ -2,13 +2,14 @@
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
 from torch.autograd.function import once_differentiable
 
 from . import _binding as base
-from ._modified import check_on, dtype_code, launch_on
+from ._modified import check_on, dtype_code, on, ptr
 
 
 def rotary_table(length: int, rotary_dim: int, base: float = 10000.0, *, scaling: str | None = None,
@@ -52,45 +53,46 @@ def rotary_table(length: int, rotary_dim: int, base: float = 10000.0, *, scaling
 def strides3(t: torch.Tensor, name: str):
     """(batch, head, token) strides in elements of a (B,H,N,D) tensor whose D columns are
     contiguous; 0 for axes of size one."""
-    if t.shape[3] > 1 and t.stride(3) != 1:
+    shape = t.shape
+    b, h, n, d = t.stride()
+    if d != 1 and shape[3] > 1:
         raise ValueError(f"{name} must have contiguous columns")
-    s = tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
-    if any(x % 8 for x in s) or t.data_ptr() % 16:
+    b, h, n = b if shape[0] > 1 else 0, h if shape[1] > 1 else 0, n if shape[2] > 1 else 0
+    if (b | h | n) & 7 or t.data_ptr() & 15:
         raise ValueError(f"{name} must be 16-byte aligned, with batch, head and token strides that are multiples "
                          f"of 8 elements; got strides {tuple(t.stride())}")
-    return s
+    return b, h, n
 
 
+@functools.lru_cache(maxsize=256)
 def c_strides(s):
-    return None if s is None else (ctypes.c_longlong * 3)(*s)
+    return (ctypes.c_longlong * 3)(*s)
 
 
 def check_strided(t, name, dtype, shape, device) -> None:
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device:
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
 def check_table(table, D, device):
     if not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("table must be a (positions, rotary columns) tensor, as rotary_table makes it")
     check_on(table, "table", torch.float32, table.shape, device)
-    R = table.shape[1]
-    if R < 2 or R % 2 or R > D or table.shape[0] < 1:
+    rows, R = table.shape
+    if R < 2 or R % 2 or R > D or rows < 1:
         raise ValueError(f"table must have an even number of columns from 2 to {D} and a row, got {tuple(table.shape)}")
     return R
 
 
-def fa_rotary(q, k, q_out, k_out, table, positions=None, interleaved: bool = False, inverse: bool = False,
-              stream=None) -> None:
-    """q_out, k_out <- q, k (bf16 or fp16 (B,H,N,D) and (B,Hkv,N,D), k or q None to leave it out)
-    with each row turned by its position; inverse turns back.  Inputs may be strided; outputs are
-    contiguous.  positions: int32 (N), (1,N) or (B,N), None: 0 .. N-1."""
+def _rotary_args(q, k, table, positions):
+    """Checks the inputs; returns (shape, heads, strides, the C call's middle arguments)."""
     some = q if q is not None else k
     if some is None:
         raise ValueError("q and k cannot both be None")
@@ -98,38 +100,58 @@ def fa_rotary(q, k, q_out, k_out, table, positions=None, interleaved: bool = Fal
     if some.dim() != 4:
         raise ValueError(f"q and k must be (B,H,N,D), got {tuple(some.shape)}")
     B, _, N, D = some.shape
-    dev = some.device
-    heads, strides = [0, 0], [None, None]
-    for i, (name, t, out) in enumerate((("q", q, q_out), ("k", k, k_out))):
-        if t is None:
-            continue
-        heads[i] = t.shape[1] if t.dim() == 4 else 0
-        check_strided(t, name, some.dtype, (B, heads[i], N, D), dev)
-        check_on(out, name + "_out", some.dtype, (B, heads[i], N, D), dev)
-        strides[i] = strides3(t, name)
+    dev, dtype = some.device, some.dtype
+    H = Hkv = 0
+    qs = ks = None
+    if q is not None:
+        H = q.shape[1]
+        qs = c_strides(strides3(q, "q"))
+    if k is not None:
+        Hkv = k.shape[1] if k.dim() == 4 else 0
+        check_strided(k, "k", dtype, (B, Hkv, N, D), dev)
+        ks = c_strides(strides3(k, "k"))
     R = check_table(table, D, dev)
     stride = 0
     if positions is not None:
-        shape = (N,) if isinstance(positions, torch.Tensor) and positions.dim() == 1 else (
-            (1, N) if isinstance(positions, torch.Tensor) and tuple(positions.shape) == (1, N) else (B, N))
+        if not isinstance(positions, torch.Tensor):
+            raise TypeError("positions must be a torch.Tensor")
+        shape = (N,) if positions.dim() == 1 else ((1, N) if positions.shape == (1, N) else (B, N))
         check_on(positions, "positions", torch.int32, shape, dev)
         stride = N if shape == (B, N) and B > 1 else 0
-    with launch_on(dev, stream):
-        base._raise(base.load_library().fa_rotary(
-            base._p(q), base._p(k), base._p(q_out if q is not None else None), base._p(k_out if k is not None else None),
-            base._p(table), base._p(positions), c_strides(strides[0]), c_strides(strides[1]), stride, table.shape[0],
-            B, heads[0], heads[1], N, D, R, int(interleaved), int(inverse), code, base._stream(None)), "fa_rotary")
+    return B, H, Hkv, N, D, R, code, dev, (ptr(positions), qs, ks, stride, table.shape[0])
+
+
+def _rotary(raw, keep, q, k, q_out, k_out, table, middle, tail):
+    base._raise(base.load_library().fa_rotary(ptr(q), ptr(k), ptr(q_out), ptr(k_out), table.data_ptr(), *middle, *tail,
+                                              raw), "fa_rotary")
+
+
+def fa_rotary(q, k, q_out, k_out, table, positions=None, interleaved: bool = False, inverse: bool = False,
+              stream=None) -> None:
+    """q_out, k_out <- q, k (bf16 or fp16 (B,H,N,D) and (B,Hkv,N,D), k or q None to leave it out)
+    with each row turned by its position; inverse turns back.  Inputs may be strided; outputs are
+    contiguous.  positions: int32 (N), (1,N) or (B,N), None: 0 .. N-1."""
+    B, H, Hkv, N, D, R, code, dev, middle = _rotary_args(q, k, table, positions)
+    dtype = (q if q is not None else k).dtype
+    if q is not None:
+        check_on(q_out, "q_out", dtype, (B, H, N, D), dev)
+    if k is not None:
+        check_on(k_out, "k_out", dtype, (B, Hkv, N, D), dev)
+    on(dev, stream, _rotary, q, k, q_out if q is not None else None, k_out if k is not None else None, table, middle,
+       (B, H, Hkv, N, D, R, int(interleaved), int(inverse), code))
 
 
 def _turn(q, k, table, positions, interleaved, inverse, stream):
-    some = q if q is not None else k
-    if some is None:
-        raise ValueError("q and k cannot both be None")
-    dtype_code(some, "q" if q is not None else "k")
-    with launch_on(some.device, stream) as keep:
-        outs = [None if t is None else keep(torch.empty(t.shape, device=t.device, dtype=t.dtype)) for t in (q, k)]
-        fa_rotary(q, k, outs[0], outs[1], table, positions, interleaved, inverse)
-    return tuple(outs)
+    B, H, Hkv, N, D, R, code, dev, middle = _rotary_args(q, k, table, positions)
+    tail = (B, H, Hkv, N, D, R, int(interleaved), int(inverse), code)
+
+    def call(raw, keep):
+        q_out = None if q is None else keep(q.new_empty(q.shape))
+        k_out = None if k is None else keep(k.new_empty(k.shape))
+        _rotary(raw, keep, q, k, q_out, k_out, table, middle, tail)
+        return q_out, k_out
+
+    return on(dev, stream, call)
 
 
 def rotary_forward(q, k, table, *, positions=None, interleaved: bool = False, stream=None):
