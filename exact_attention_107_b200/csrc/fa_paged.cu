@@ -38,7 +38,7 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kThreads = 192;        // warps 0-3: softmax; 4: loads; 5: MMA
+constexpr int kThreads = 224;        // warps 0-3: softmax; 4: Q and K loads; 5: MMA; 6: V loads
 constexpr int kTile = 128;           // positions a tile
 constexpr int kBox = kTile * 128;    // bytes of 64 columns of a tile
 constexpr int kMaxCtas = 148;
@@ -51,20 +51,28 @@ constexpr int tile_dim(int D) { return D <= 64 ? 64 : (D <= 128 ? 128 : 256); }
 template <int D, int R>
 struct Smem {
   static constexpr int kDP = tile_dim(D);
-  static constexpr int kNBox = kDP / 64;
-  static constexpr int kSlot = kNBox * kBox;
+  static constexpr int kNBox = kDP / 64;                            // 64-column boxes of a tile
+  static constexpr int kParts = kDP == 256 ? 2 : 1;                 // a tile's slots: up to 128 columns each
+  static constexpr int kPartBoxes = kNBox / kParts;
+  static constexpr int kSlot = kPartBoxes * kBox;
   static constexpr int kQ = kNBox * R * 128;
   static constexpr int kP = 2 * R * 128;
   static constexpr int kBufs = (kDP == 256 && R > 16) ? 1 : 2;     // Q and P buffers
   static constexpr int kRing = 227 * 1024 - 4096 - kBufs * (kQ + kP);
   static constexpr int kSlots = kRing / kSlot < 12 ? kRing / kSlot : 12;
+  // K and V have a ring each, with one warp that fills it in order and the MMA warp that empties it
+  // in order: every parity is then waited for at most one phase ahead.
+  static constexpr int kKSlots = (kSlots + 1) / 2, kVSlots = kSlots / 2;
+  static constexpr int kOffV = kKSlots * kSlot;
   static constexpr int kOffQ = kSlots * kSlot;
   static constexpr int kOffP = kOffQ + kBufs * kQ;
   static constexpr int kOffRows = kOffP + kBufs * kP;               // int4 (position, first, slope2, -) per row
   static constexpr int kOffMax = kOffRows + R * 16;                 // float [2][R][4]: the warps' maxima
   static constexpr int kOffRef = kOffMax + 2 * R * 16;              // float [R] reference maximum, [R] factor
-  static constexpr int kOffBar = kOffRef + 2 * R * 4;
-  static constexpr int kBarFull = 0, kBarEmpty = kSlots, kBarQFull = 2 * kSlots, kBarQEmpty = kBarQFull + 2;
+  static constexpr int kOffFlags = kOffRef + 2 * R * 4;             // int [2][4]
+  static constexpr int kOffBar = kOffFlags + 32;
+  static constexpr int kBarKFull = 0, kBarKEmpty = kKSlots, kBarVFull = 2 * kKSlots, kBarVEmpty = kBarVFull + kVSlots;
+  static constexpr int kBarQFull = 2 * kSlots, kBarQEmpty = kBarQFull + 2;
   static constexpr int kBarSFull = kBarQEmpty + 2, kBarSEmpty = kBarSFull + 2;
   static constexpr int kBarPFull = kBarSEmpty + 2, kBarPEmpty = kBarPFull + 2, kBarDone = kBarPEmpty + 2,
                        kBarSync = kBarDone + 1;
@@ -74,7 +82,7 @@ struct Smem {
   static constexpr int kEnd = kOffMisc + 128;
   static constexpr int kBytes = (kEnd > kOffQ + kBox ? kEnd : kOffQ + kBox) + 1024;
   static constexpr int kTmemCols = 2 * R + R * (kDP == 256 ? 2 : 1) <= 64 ? 64 : (R <= 32 ? 128 : 256);
-  static_assert(kSlots >= 3 && kBytes <= 227 * 1024, "shared memory");
+  static_assert(kVSlots >= 2 && kVSlots >= kParts && kBytes <= 227 * 1024, "shared memory");
 };
 
 // The call's shape as the kernels use it.
@@ -156,8 +164,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto bar = [&](int i) { return sb + L::kOffBar + 8u * i; };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
-  long long* scan = reinterpret_cast<long long*>(smem + L::kOffMisc + 8);      // [8]
-  int* found = reinterpret_cast<int*>(smem + L::kOffMisc + 72);                // sequence; then its first tile
+  long long* scan = reinterpret_cast<long long*>(smem + L::kOffMisc + 8);      // [7]
+  int* found = reinterpret_cast<int*>(smem + L::kOffMisc + 72);                // the piece's first sequence
   long long* found_at = reinterpret_cast<long long*>(smem + L::kOffMisc + 80);
   int4* rows = reinterpret_cast<int4*>(smem + L::kOffRows);
   float* ref = reinterpret_cast<float*>(smem + L::kOffRef);
@@ -165,10 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Workspace ws = workspace_view<DP, R>(a.workspace);
 
   if (tid == 0) {
-    for (int i = 0; i < L::kSlots; ++i) {
-      mbar_init(bar(L::kBarFull + i), 1);
-      mbar_init(bar(L::kBarEmpty + i), 1);
-    }
+    for (int i = 0; i < 2 * L::kSlots; ++i) mbar_init(bar(i), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(L::kBarQFull + i), 1);
       mbar_init(bar(L::kBarQEmpty + i), 1);
@@ -259,10 +264,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     w.tile = static_cast<int>(*found_at % w.s.ntiles);
   }
 
-  if (warp == 4) {
+  if (warp == 4 || warp == 6) {
     // ------------------------------------------------------------------ loads
+    // A box of a small page takes its lane some hundred clocks to issue, so K and V have a warp each.
+    const int kv = warp == 4 ? 0 : 1;
+    const CUtensorMap* map = kv == 0 ? &tmK : &tmV;
+    const int slots = kv == 0 ? L::kKSlots : L::kVSlots, full = kv == 0 ? L::kBarKFull : L::kBarVFull,
+              empty = kv == 0 ? L::kBarKEmpty : L::kBarVEmpty;
+    const uint32_t ring = sb + (kv == 0 ? 0 : L::kOffV);
     const int box_rows = min(kTile, 1 << a.page_shift), pages = kTile / box_rows;
-    int fills = 0, u = 0, loaded_q = 0;
+    int fills = 0, u = 0;
     bool ok = true;
     // This lane's page of a tile: the pool row of its first position, or -1.
     auto lookup = [&](const Walk& w, int tile) {
@@ -278,17 +289,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int row = w.more() ? lookup(w, w.tile) : -1;
     while (ok && w.more()) {
-      const int qbuf = u % L::kBufs;
-      ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQEmpty + qbuf), ((u / L::kBufs) & 1) ^ 1, abort_flag));
-      if (!ok) break;
-      if (lane == 0) {
-        const int hk = w.unit / geo.groups, group = w.unit % geo.groups;
-        const int q_row = (w.b * a.H + hk * (a.H / a.Hkv)) * a.T + group * R;
-        mbar_arrive_expect_tx(bar(L::kBarQFull + qbuf), L::kQ);
-        for (int c = 0; c < L::kNBox; ++c)
-          tma_load_3d(sb + L::kOffQ + qbuf * L::kQ + c * R * 128, &tmQ, bar(L::kBarQFull + qbuf), c * 64, q_row, 0);
+      if (kv == 0) {
+        const int qbuf = u % L::kBufs;
+        ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQEmpty + qbuf), ((u / L::kBufs) & 1) ^ 1, abort_flag));
+        if (!ok) break;
+        if (lane == 0) {
+          const int hk = w.unit / geo.groups, group = w.unit % geo.groups;
+          const int q_row = (w.b * a.H + hk * (a.H / a.Hkv)) * a.T + group * R;
+          mbar_arrive_expect_tx(bar(L::kBarQFull + qbuf), L::kQ);
+          for (int c = 0; c < L::kNBox; ++c)
+            tma_load_3d(sb + L::kOffQ + qbuf * L::kQ + c * R * 128, &tmQ, bar(L::kBarQFull + qbuf), c * 64, q_row, 0);
+        }
+        ++u;
       }
-      ++loaded_q;
       const int end = w.tile + w.count();
       for (int t = w.tile; ok && t < end; ++t) {
         const int cur = row;
@@ -300,34 +313,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           row = n.more() ? lookup(n, n.tile) : -1;
         }
         const unsigned valid = __ballot_sync(0xffffffffu, cur >= 0);
-        const uint32_t bytes = static_cast<uint32_t>(__popc(valid)) * box_rows * 128 * L::kNBox;
+        const uint32_t bytes = static_cast<uint32_t>(__popc(valid)) * box_rows * 128 * L::kPartBoxes;
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          const int slot = fills % L::kSlots;
-          ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarEmpty + slot), ((fills / L::kSlots) & 1) ^ 1, abort_flag));
+        for (int part = 0; part < L::kParts; ++part) {
+          const int slot = fills % slots;
+          ok = __all_sync(0xffffffffu, mbar_wait(bar(empty + slot), ((fills / slots) & 1) ^ 1, abort_flag));
           if (!ok) break;
           if (lane == 0) {
-            if (bytes > 0) mbar_arrive_expect_tx(bar(L::kBarFull + slot), bytes);
-            else mbar_arrive(bar(L::kBarFull + slot));
+            if (bytes > 0) mbar_arrive_expect_tx(bar(full + slot), bytes);
+            else mbar_arrive(bar(full + slot));
           }
           __syncwarp();
           if (cur >= 0) {
-            for (int c = 0; c < L::kNBox; ++c)
-              tma_load_3d(sb + slot * L::kSlot + c * kBox + lane * box_rows * 128, kv == 0 ? &tmK : &tmV,
-                          bar(L::kBarFull + slot), c * 64, cur, 0);
+#pragma unroll
+            for (int c = 0; c < L::kPartBoxes; ++c)
+              tma_load_3d(ring + slot * L::kSlot + c * kBox + lane * box_rows * 128, map, bar(full + slot),
+                          (part * L::kPartBoxes + c) * 64, cur, 0);
           }
           ++fills;
         }
       }
       w.next(a, geo.units);
-      ++u;
     }
     __syncwarp();
     if (!ok) {
       if (lane == 0) raise_error(a.status, abort_flag, kStatusTimeout);
-      for (int f = max(0, fills - L::kSlots); f < fills; ++f)
-        mbar_wait_drain(bar(L::kBarFull + f % L::kSlots), (f / L::kSlots) & 1);
-      for (int q = max(0, loaded_q - L::kBufs); q < loaded_q; ++q)
+      for (int f = max(0, fills - slots); f < fills; ++f) mbar_wait_drain(bar(full + f % slots), (f / slots) & 1);
+      for (int q = max(0, u - L::kBufs); q < u; ++q)
         mbar_wait_drain(bar(L::kBarQFull + q % L::kBufs), (q / L::kBufs) & 1);
     }
   } else if (warp == 5) {
@@ -335,48 +347,67 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0 && w.more()) {
       constexpr uint32_t kIdS = idesc_16(128, R, false, false, F16);
       constexpr uint32_t kIdO = idesc_16(128, R, true, false, F16);        // A = V^T: MN-major
-      int i = 0, u = 0;
-      bool first_pv = true, ok = true;       // of PV(i - 1): the unit's first tile
-      auto pv = [&](int j, bool first) {
-        const int pbuf = j % L::kBufs, slot = (2 * j + 1) % L::kSlots;
-        if (!mbar_wait_spin(bar(L::kBarPFull + pbuf), (j / L::kBufs) & 1, abort_flag)) return false;
-        if (!mbar_wait_spin(bar(L::kBarFull + slot), ((2 * j + 1) / L::kSlots) & 1, abort_flag)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < (DP + 127) / 128; ++h)
+      const int n = static_cast<int>(w.left);
+      int is = 0, ip = 0, u = 0;             // next S^T, next P V, unit of the next S^T
+      int ks = 0, vs = 0;                    // parts of K and V taken so far (kParts a tile)
+      int unit_end = w.count();              // first tile of the next unit
+      uint32_t firsts = 1u;                  // bit i % 32: tile i is its unit's first
+      bool ok = true;
+      long long t0 = clock64();
+      // Whichever product has its operands goes next; P V first, as it frees a slot.
+      while (ip < n) {
+        const int pbuf = ip % L::kBufs, vslot = vs % L::kVSlots, vpart = vs % L::kParts;
+        if (ip < is && (vpart > 0 || mbar_test_wait(bar(L::kBarPFull + pbuf), (ip / L::kBufs) & 1)) &&
+            mbar_test_wait(bar(L::kBarVFull + vslot), (vs / L::kVSlots) & 1)) {
+          tc_fence_after();
+          const uint32_t keep = (firsts >> (ip & 31)) & 1u ? 0u : 1u;
 #pragma unroll
           for (int g = 0; g < 2; ++g)
             mma_ss_x4<128, 256, 384, 2, 4, 6>(
-                tmem + 2 * R + h * R, sdesc_sw128(sb + slot * L::kSlot + h * 2 * kBox + g * 4 * 2048, kBox, 1024),
-                sdesc_sw128(sb + L::kOffP + pbuf * L::kP + g * R * 128, 16, 1024), kIdO, (first && g == 0) ? 0u : 1u);
-        tc_commit(bar(L::kBarPEmpty + pbuf));
-        tc_commit(bar(L::kBarEmpty + slot));
-        return true;
-      };
-      while (ok && w.more()) {
-        const int qbuf = u % L::kBufs, n = w.count();
-        if (!(ok = mbar_wait_spin(bar(L::kBarQFull + qbuf), (u / L::kBufs) & 1, abort_flag))) break;
-        for (int t = 0; t < n; ++t, ++i) {
-          const int slot = (2 * i) % L::kSlots, sbuf = i & 1;
-          if (!(ok = mbar_wait_spin(bar(L::kBarFull + slot), ((2 * i) / L::kSlots) & 1, abort_flag))) break;
-          if (!(ok = mbar_wait_spin(bar(L::kBarSEmpty + sbuf), ((i >> 1) & 1) ^ 1, abort_flag))) break;
+                tmem + 2 * R + vpart * R, sdesc_sw128(sb + L::kOffV + vslot * L::kSlot + g * 4 * 2048, kBox, 1024),
+                sdesc_sw128(sb + L::kOffP + pbuf * L::kP + g * R * 128, 16, 1024), kIdO, g == 0 ? keep : 1u);
+          tc_commit(bar(L::kBarVEmpty + vslot));
+          ++vs;
+          if (vpart == L::kParts - 1) {
+            tc_commit(bar(L::kBarPEmpty + pbuf));
+            ++ip;
+          }
+          t0 = clock64();
+          continue;
+        }
+        const int kslot = ks % L::kKSlots, kpart = ks % L::kParts, sbuf = is & 1, qbuf = u % L::kBufs;
+        if (is < n && mbar_test_wait(bar(L::kBarKFull + kslot), (ks / L::kKSlots) & 1) &&
+            (kpart > 0 || (mbar_test_wait(bar(L::kBarSEmpty + sbuf), ((is >> 1) & 1) ^ 1) &&
+                           mbar_test_wait(bar(L::kBarQFull + qbuf), (u / L::kBufs) & 1)))) {
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < L::kNBox; ++c)
-            mma_ss_x4<2, 4, 6, 2, 4, 6>(tmem + sbuf * R, sdesc_sw128(sb + slot * L::kSlot + c * kBox, 16, 1024),
-                                        sdesc_sw128(sb + L::kOffQ + qbuf * L::kQ + c * R * 128, 16, 1024), kIdS,
-                                        c > 0 ? 1u : 0u);
-          tc_commit(bar(L::kBarSFull + sbuf));
-          tc_commit(bar(L::kBarEmpty + slot));
-          if (t + 1 == n) tc_commit(bar(L::kBarQEmpty + qbuf));
-          if (i > 0 && !(ok = pv(i - 1, first_pv))) break;
-          first_pv = t == 0;
+          for (int c = 0; c < L::kPartBoxes; ++c)
+            mma_ss_x4<2, 4, 6, 2, 4, 6>(
+                tmem + sbuf * R, sdesc_sw128(sb + kslot * L::kSlot + c * kBox, 16, 1024),
+                sdesc_sw128(sb + L::kOffQ + qbuf * L::kQ + (kpart * L::kPartBoxes + c) * R * 128, 16, 1024), kIdS,
+                (c > 0 || kpart > 0) ? 1u : 0u);
+          tc_commit(bar(L::kBarKEmpty + kslot));
+          ++ks;
+          if (kpart == L::kParts - 1) {
+            tc_commit(bar(L::kBarSFull + sbuf));
+            ++is;
+            firsts &= ~(1u << (is & 31));
+            if (is == unit_end) {
+              tc_commit(bar(L::kBarQEmpty + qbuf));
+              firsts |= 1u << (is & 31);
+              ++u;
+              w.next(a, geo.units);
+              unit_end = w.more() ? is + w.count() : n + 1;
+            }
+          }
+          t0 = clock64();
+          continue;
         }
-        if (!ok) break;
-        w.next(a, geo.units);
-        ++u;
+        if (*abort_flag || clock64() - t0 > kWaitLimitCycles) {
+          ok = false;
+          break;
+        }
       }
-      if (ok && i > 0) ok = pv(i - 1, first_pv);
       if (!ok) raise_error(a.status, abort_flag, kStatusTimeout);
       tc_commit(bar(L::kBarDone));
       mbar_wait_drain(bar(L::kBarDone), 0);
@@ -482,19 +513,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         float* wmax = reinterpret_cast<float*>(smem + L::kOffMax) + (i & 1) * 4 * R;
         share_row(wmax, mine, mine2);
+        // does a row of this warp's outgrow its reference?  (lane: its own rows)
+        const bool mine_grew = (lane < R && mine > ref[lane % R] + kRescale) || (R > 32 && mine2 > ref[(lane + 32) % R] + kRescale);
+        const bool grew = __any_sync(0xffffffffu, mine_grew);
+        int* flags = reinterpret_cast<int*>(smem + L::kOffFlags) + (i & 1) * 4;
+        if (lane == 0) flags[warp] = grew;
         if (!(ok = sync())) break;
-        auto top = [&](int n) {
-          const float4 v = *reinterpret_cast<const float4*>(wmax + 4 * n);
-          return fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-        };
-        bool need = false;
-#pragma unroll
-        for (int n = 0; n < R; ++n) need |= top(n) > ref[n] + kRescale;
-        // every thread sees the same maxima, so the branch is uniform
-        if (need) {
-          if (!(ok = sync())) break;
+        const int4 any = *reinterpret_cast<const int4*>(flags);
+        // every thread reads the same flags, so the branch is uniform
+        if (any.x | any.y | any.z | any.w) {
           if (tid < R) {
-            const float was = ref[tid], now = fmaxf(was, top(tid));
+            const float4 v = *reinterpret_cast<const float4*>(wmax + 4 * tid);
+            const float was = ref[tid], now = fmaxf(was, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
             ref[R + tid] = now == -CUDART_INF_F ? 1.f : ex2_approx(was - now);
             ref[tid] = now;
           }
@@ -531,55 +561,85 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint8_t* p_at = smem + L::kOffP + (i % L::kBufs) * L::kP + (tid >> 6) * (R * 128) + (tid & 7) * 2;
         const int chunk = (tid & 63) >> 3;
 #pragma unroll
-        for (int n = 0; n < R; ++n) {
-          const float m = ref[n];
-          const float p = ex2_approx(X(n) - (m == -CUDART_INF_F ? 0.f : m));
-          l[n] += p;
-          *reinterpret_cast<uint16_t*>(p_at + n * 128 + ((chunk ^ (n & 7)) << 4)) = static_cast<uint16_t>(pack16<F16>(p, 0.f));
-        }
-        if (!live) {
-          const int f = 2 * i + 1, slot = f % L::kSlots;
-          // no __all_sync: lanes of one warp differ, and the wait is the thread's own
-          if (mbar_wait(bar(L::kBarFull + slot), (f / L::kSlots) & 1, abort_flag)) {
+        for (int c = 0; c < R; c += 16) {
+          float m[16];
 #pragma unroll
-            for (int c = 0; c < L::kNBox; ++c)
+          for (int e = 0; e < 16; e += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(ref + c + e);
+            m[e] = v.x, m[e + 1] = v.y, m[e + 2] = v.z, m[e + 3] = v.w;
+          }
+          uint16_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float p = ex2_approx(X(c + e) - (m[e] == -CUDART_INF_F ? 0.f : m[e]));
+            l[c + e] += p;
+            pk[e] = static_cast<uint16_t>(pack16<F16>(p, 0.f));
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            *reinterpret_cast<uint16_t*>(p_at + (c + e) * 128 + ((chunk ^ (e & 7)) << 4)) = pk[e];
+        }
+        if (__any_sync(0xffffffffu, !live)) {
+          // V rows that nothing may see.  The tile's V has landed in its slots only if an earlier
+          // tile's is out of them, so the product before comes first.
+          if (i > 0) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarPEmpty + (i - 1) % L::kBufs), ((i - 1) / L::kBufs) & 1, abort_flag));
+#pragma unroll
+          for (int part = 0; part < L::kParts; ++part) {
+            const int f = i * L::kParts + part, slot = f % L::kVSlots;
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(bar(L::kBarVFull + slot), (f / L::kVSlots) & 1, abort_flag));
+            if (!ok) break;
+            if (live) continue;
+#pragma unroll
+            for (int c = 0; c < L::kPartBoxes; ++c)
 #pragma unroll
               for (int q = 0; q < 8; ++q)
-                *reinterpret_cast<uint4*>(smem + slot * L::kSlot + c * kBox + tid * 128 + q * 16) = make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(smem + L::kOffV + slot * L::kSlot + c * kBox + tid * 128 + q * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
+          if (!ok) break;
         }
         __syncwarp();
         fence_async_smem();
         mbar_arrive(bar(L::kBarPFull + i % L::kBufs));
       }
       if (!ok) break;
-      // The unit's end in this piece: sums over the keys' threads, O^T (lane = column of O).
+      // The unit's end in this piece.  Sums over the keys' threads: each step of the butterfly
+      // halves the rows that a lane holds, so lane i is left with row i / (32 / R) (R = 64: two).
 #pragma unroll
-      for (int n = 0; n < R; ++n) {
+      for (int d = 16, h = R / 2; d > 0; d >>= 1, h >>= 1) {
+        if (h >= 1) {
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], d);
+          for (int n = 0; n < R / 2; ++n) {
+            if (n >= h) break;
+            const bool up = (lane & d) != 0;
+            const float give = up ? l[n] : l[n + h], keep = up ? l[n + h] : l[n];
+            l[n] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+          }
+        } else {
+          l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
+        }
       }
-      if (!(ok = sync())) break;  // the maxima are read
+      if (!(ok = sync())) break;                         // the maxima are read
       float* wsum = reinterpret_cast<float*>(smem + L::kOffMax);
-      float mine = 0.f, mine2 = 0.f;
 #pragma unroll
-      for (int n = 0; n < R; ++n) {
-        if (n < 32) mine = lane == n ? l[n] : mine;
-        else mine2 = lane == n - 32 ? l[n] : mine2;
-      }
-      share_row(wsum, mine, mine2);
+      for (int n = 0; n < (R > 32 ? 2 : 1); ++n)
+        if (R >= 32 || lane % (R >= 32 ? 1 : 32 / R) == 0) wsum[((R >= 32 ? lane * (R / 32) : lane / (R >= 32 ? 1 : 32 / R)) + n) * 4 + warp] = l[n];
       if (!(ok = sync())) break;
-#pragma unroll
-      for (int n = 0; n < R; ++n) {
-        const float4 v = *reinterpret_cast<const float4*>(wsum + 4 * n);
-        l[n] = (v.x + v.y) + (v.z + v.w);
+      const bool whole = n_tiles == w.s.ntiles;
+      const int part = static_cast<int>(blockIdx.x) * 2 + (w.tile == 0 ? 1 : 0);
+      if (tid < R) {
+        const float4 v = *reinterpret_cast<const float4*>(wsum + 4 * tid);
+        const float total_l = (v.x + v.y) + (v.z + v.w), m = ref[tid];
+        ref[R + tid] = !whole ? 1.f : (total_l == 0.f ? 0.f : 1.f / total_l);
+        if (tid < rows_here) {
+          if (whole) a.lse[q_row + tid] = total_l == 0.f ? -CUDART_INF_F : (m + log2f(total_l)) * kLn2;
+          else ws.stats[part * R + tid] = make_float2(m, total_l);
+        }
       }
+      if (!(ok = sync())) break;
       ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarPEmpty + (i - 1) % L::kBufs), ((i - 1) / L::kBufs) & 1, abort_flag));
       if (!ok) break;
       FA_CONVERGED(a.status);
       tc_fence_after();
-      const bool whole = n_tiles == w.s.ntiles;
-      const int part = static_cast<int>(blockIdx.x) * 2 + (w.tile == 0 ? 1 : 0);
 #pragma unroll
       for (int h = 0; h < (DP + 127) / 128; ++h) {
         const int d = h * 128 + tid;
@@ -590,26 +650,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld16(tmem + quad + 2 * R + h * R + c, o);
           tmem_ld_wait();
           reg_fence(o);
+          float f[16];
+#pragma unroll
+          for (int e = 0; e < 16; e += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(ref + R + c + e);
+            f[e] = v.x, f[e + 1] = v.y, f[e + 2] = v.z, f[e + 3] = v.w;
+          }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int n = c + e;
             if (n >= rows_here || d >= D) continue;
-            if (whole) {
-              const float inv = l[n] == 0.f ? 0.f : 1.f / l[n];
-              a.o[(q_row + n) * D + d] = static_cast<uint16_t>(pack16<F16>(__uint_as_float(o[e]) * inv, 0.f));
-            } else {
-              ws.part[(static_cast<size_t>(part) * R + n) * DP + d] = __uint_as_float(o[e]);
-            }
+            const float value = __uint_as_float(o[e]) * f[e];
+            if (whole) a.o[(q_row + n) * D + d] = static_cast<uint16_t>(pack16<F16>(value, 0.f));
+            else ws.part[(static_cast<size_t>(part) * R + n) * DP + d] = value;
           }
         }
       }
       tc_fence_before();
-#pragma unroll
-      for (int n = 0; n < R; ++n) {
-        if (tid != n || n >= rows_here) continue;
-        if (whole) a.lse[q_row + n] = l[n] == 0.f ? -CUDART_INF_F : (ref[n] + log2f(l[n])) * kLn2;
-        else ws.stats[part * R + n] = make_float2(ref[n], l[n]);
-      }
       if (!whole && w.tile == 0 && tid == 0) {
         // the pieces behind this one that hold the rest
         const long long rest = w.s.ntiles - n_tiles;
@@ -627,13 +684,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Joins the pieces of the unit that begins in CTA blockIdx.x's piece, row blockIdx.y: the four warps
-// take every fourth piece, a lane D / 32 columns.
+// Joins the pieces of the unit that begins in CTA blockIdx.x's piece, row blockIdx.y.  Every warp
+// finds the common maximum and the sum over all pieces, a lane for each; the eight warps take every
+// eighth piece's O, a lane D / 32 columns.
+constexpr int kJoinWarps = 8;
 template <int D, int R, bool F16>
-__global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__ PagedLaunch a,
-                                                         const __grid_constant__ Geometry geo) {
+__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedLaunch a,
+                                                                     const __grid_constant__ Geometry geo) {
   constexpr int DP = tile_dim(D), E = D / 32;
-  __shared__ float sh_o[4][D], sh_m[4], sh_l[4];
+  __shared__ float sh_o[kJoinWarps][D];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Workspace ws = workspace_view<DP, R>(a.workspace);
   const Split s = ws.splits[blockIdx.x];
@@ -642,32 +701,44 @@ __global__ void __launch_bounds__(128) paged_join_kernel(const __grid_constant__
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // piece 0 is this CTA's second part, the others are the next CTAs' first
   auto part = [&](int i) { return (static_cast<int>(blockIdx.x) + i) * 2 + (i == 0 ? 1 : 0); };
+  constexpr int kMost = (kMaxCtas + 31) / 32;
+  float2 st[kMost];
   float m = -CUDART_INF_F, l = 0.f, o[E] = {};
-  for (int i = warp; i < s.pieces; i += 4) m = fmaxf(m, ws.stats[part(i) * R + n].x);
-  if (lane == 0) sh_m[warp] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(sh_m[0], sh_m[1]), fmaxf(sh_m[2], sh_m[3]));
-  if (m != -CUDART_INF_F) {
-#pragma unroll 4
-    for (int i = warp; i < s.pieces; i += 4) {
-      const float2 st = ws.stats[part(i) * R + n];
-      const float* p = ws.part + (static_cast<size_t>(part(i)) * R + n) * DP;
-      const float f = ex2_approx(st.x - m);
-      l = fmaf(f, st.y, l);
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(f, p[e * 32 + lane], o[e]);
+  for (int c = 0; c < kMost; ++c) {
+    st[c] = c * 32 + lane < s.pieces ? ws.stats[part(c * 32 + lane) * R + n] : make_float2(-CUDART_INF_F, 0.f);
+    m = fmaxf(m, st[c].x);
+  }
+  m = redux_max(m);
+  if (m != -CUDART_INF_F) {
+#pragma unroll
+    for (int c = 0; c < kMost; ++c) {
+      st[c].x = ex2_approx(st[c].x - m);                       // the piece's factor
+      l = fmaf(st[c].x, st[c].y, l);
+#pragma unroll
+      for (int k = 0; k < 32 / kJoinWarps; ++k) {
+        const int at = warp + k * kJoinWarps, i = c * 32 + at;
+        const float f = __shfl_sync(0xffffffffu, st[c].x, at);
+        if (i >= s.pieces) continue;
+        const float* p = ws.part + (static_cast<size_t>(part(i)) * R + n) * DP;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(f, p[e * 32 + lane], o[e]);
+      }
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) sh_o[warp][e * 32 + lane] = o[e];
-  if (lane == 0) sh_l[warp] = l;
   __syncthreads();
-  l = (sh_l[0] + sh_l[1]) + (sh_l[2] + sh_l[3]);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const long long row = (static_cast<long long>(s.b) * a.H + s.unit / geo.groups * (a.H / a.Hkv)) * a.T + r0 + n;
-  for (int d = threadIdx.x; d < D; d += 128)
-    a.o[row * D + d] = static_cast<uint16_t>(
-        pack16<F16>(((sh_o[0][d] + sh_o[1][d]) + (sh_o[2][d] + sh_o[3][d])) * inv, 0.f));
+  for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) sum += sh_o[w][d];
+    a.o[row * D + d] = static_cast<uint16_t>(pack16<F16>(sum * inv, 0.f));
+  }
   if (threadIdx.x == 0) a.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
 }
 
@@ -697,7 +768,7 @@ cudaError_t launch_impl(const PagedLaunch& a, cudaStream_t stream) {
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(ctas, geo.M < R ? geo.M : R);
-  cfg.blockDim = dim3(128);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -195,6 +195,16 @@ DECODE = [
     (2, 9, 1, 3, 256, 64, [4097, 65], 0.0, False, 0, "bf16"),
     (130, 2, 1, 1, 64, 16, [n % 97 for n in range(130)], 0.0, False, 0, "fp16"),
     (1, 8, 8, 1, 96, 32, [3001], 0.0, True, 1000, "bf16"),
+    # several tiles and units for each CTA, every head dim and group size
+    (6, 16, 8, 1, 256, 32, [3000, 700, 2500, 0, 1500, 129], 0.0, False, 0, "bf16"),
+    (6, 32, 8, 3, 256, 16, [2600, 2900, 1, 2000, 256, 1100], 0.0, True, 1000, "fp16"),
+    (5, 40, 4, 3, 256, 64, [4500, 5000, 300, 3000, 2047], 30.0, False, 0, "bf16"),
+    (4, 64, 8, 4, 128, 16, [4000, 2222, 3333, 90], 0.0, False, 0, "bf16"),
+    (3, 64, 8, 8, 128, 32, [2000, 5000, 3500], 0.0, True, 0, "fp16"),
+    (6, 16, 16, 1, 64, 8, [2000, 100, 3000, 1, 0, 1777], 0.0, False, 0, "bf16"),
+    (5, 16, 16, 2, 32, 128, [2500, 128, 3000, 4000, 127], 20.0, False, 700, "fp16"),
+    (4, 48, 16, 1, 96, 256, [3000, 2560, 255, 1025], 0.0, False, 0, "bf16"),
+    (2, 32, 8, 13, 64, 64, [6000, 4100], 0.0, False, 0, "bf16"),
 ]
 
 
