@@ -8,13 +8,11 @@
 // columns R.. are copied.  The gradient is the transpose: sin changes sign (`inverse`).  Products
 // and sums are fp32, rounded once.
 //
-// Bound by memory: every element is read once and written once (16-byte loads and stores), the
-// table row from L1 / L2.  Work is laid out over (token, head, unit): a unit is 8 columns
-// (interleaved, or a half layout whose halves do not split into 8s, where the partner columns are
-// read one by one from L1), or 8 + 8 partner columns (half layout with R a multiple of 16).
-// Consecutive threads take consecutive units, then heads of one token, which is the order of
-// token-major inputs; each thread handles up to kHeads heads of its token, so the angles are read
-// and unpacked once and several loads are in flight.
+// Bound by memory: every element is read once and written once (16-byte accesses), the table row
+// from L1 / L2.  A unit of a row is 8 columns, or 8 and their 8 partners (half layout with R a
+// multiple of 16).  A thread keeps one unit of one token: it unpacks the angles once and turns up
+// to kHeads heads of the token at a time, so that many loads are in flight.  Threads are laid out
+// (unit, head, token): in a token-major input neighbouring threads read neighbouring bytes.
 #include <cstdint>
 
 #include "fa_internal.h"
@@ -25,8 +23,14 @@ namespace fa {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kHeads = 4;
 
-enum Layout { kHalfWide = 0, kInterleaved = 1, kHalfOdd = 2 };
+// How the pairs of a unit lie.
+//   kHalfWide     half layout, R a multiple of 16: the thread holds both columns of its pairs
+//   kInterleaved  pairs are neighbours; R a multiple of 8, so a unit turns whole or not at all
+//   kHalfOdd, kInterleavedOdd   other R: the angles are read one by one, and the half layout's
+//                 partners come out of shared memory, where the block leaves its rows
+enum Layout { kHalfWide = 0, kInterleaved = 1, kHalfOdd = 2, kInterleavedOdd = 3 };
 
 template <bool F16>
 __device__ __forceinline__ void unpack8(const uint4& x, float (&f)[8]) {
@@ -41,175 +45,188 @@ template <bool F16>
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack16<F16>(f[0], f[1]), pack16<F16>(f[2], f[3]), pack16<F16>(f[4], f[5]), pack16<F16>(f[6], f[7]));
 }
-template <bool F16>
-__device__ __forceinline__ float load16(const uint16_t* p) {
-  return unpack16_lo<F16>(static_cast<uint32_t>(*p));
+__device__ __forceinline__ void load8(const float* p, float (&f)[8]) {
+  const float4 x = *reinterpret_cast<const float4*>(p), y = *reinterpret_cast<const float4*>(p + 4);
+  f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w;
+  f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
 }
 
 // The heads of a token: `H` query heads, then `Hkv` key heads, then (paged) `Hkv` value heads.
-template <int LAYOUT, bool F16, bool PAGED, int HEADS>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryLaunch a, int tokens_per_block,
-                                                          int units, int head_lanes) {
+template <int LAYOUT, bool F16, bool PAGED>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryLaunch a) {
+  extern __shared__ uint4 staged[];                            // kHalfOdd: [token][head lane][kHeads][unit]
+  constexpr bool kWide = LAYOUT == kHalfWide;
+  const int u = threadIdx.x, lanes = blockDim.y;
   const int heads = a.H + a.Hkv * (PAGED ? 2 : 1);
-  const int width = head_lanes * units;                        // work items of a token
-  const int tokens = a.B * a.N;
-  const int rot_units = LAYOUT == kHalfWide ? a.R / 16 : units;
-  for (int l = threadIdx.x; l < tokens_per_block * width; l += kThreads) {
-    const int tok = static_cast<int>(blockIdx.x) * tokens_per_block + l / width;
-    if (tok >= tokens) return;
-    const int item = l % width;
-    const int head0 = item / units, u = item % units;
-    const int b = tok / a.N, n = tok % a.N;
+  const unsigned tok = blockIdx.x * blockDim.z + threadIdx.z;
+  const bool here = tok < static_cast<unsigned>(a.B) * static_cast<unsigned>(a.N);
+  if (LAYOUT != kHalfOdd && !here) return;
+  const int b = here ? static_cast<int>(tok / static_cast<unsigned>(a.N)) : 0;
+  const int n = here ? static_cast<int>(tok - static_cast<unsigned>(b) * static_cast<unsigned>(a.N)) : 0;
+  const int half = a.R / 2, rot_units = kWide ? a.R / 16 : (a.R + 7) / 8;
+  const int col0 = kWide && u >= rot_units ? 8 * u + half : 8 * u;
+  const bool pair = kWide && u < rot_units;                    // this thread holds columns col0 and col0 + half
 
-    // position, and where the token's key and value go
-    bool real = true;                                          // false: a row behind its sequence's last
-    long long p = n;
-    long long page_row = 0;                                    // (page * Hkv) * page_size + slot
-    bool write = true;
-    if (PAGED) {
-      const AppendSlot at = append_slot(a.seq_lens[b], a.new_lens != nullptr ? a.new_lens[b] : a.N, a.N, n,
-                                        a.block_table + static_cast<long long>(b) * a.table_width, a.table_width,
-                                        a.page_shift, a.num_pages);
-      real = at.real;
-      p = at.position;
-      write = at.page >= 0;
-      page_row = page_row_of(at.page, a.Hkv, 0, p, a.page_shift);
-      if (real && !write) atomicCAS(a.status, 0, kStatusIndex);
-    } else if (a.positions != nullptr) {
-      p = a.positions[static_cast<long long>(b) * a.position_stride + n];
-    }
-    // A position outside the table is reported and left unturned.
-    bool turn = u < rot_units && a.R > 0 && real;
-    if (turn && (p < 0 || p >= a.table_rows)) {
-      atomicCAS(a.status, 0, kStatusIndex);
-      turn = false;
-    }
-    float c[8], s[8];
-    const float* row = a.table + (turn ? p * a.R : 0);
-    if (LAYOUT == kHalfWide) {
-      if (turn) {
+  const int fresh = PAGED && a.new_lens != nullptr ? a.new_lens[b] : a.N;
+  uint4 x[kHeads], y[kHeads];
+  bool on[kHeads];
+  const long long q_at = b * a.q_stride[0] + n * a.q_stride[2] + col0;
+  const long long k_at = b * a.k_stride[0] + n * a.k_stride[2] + col0;
+  const long long v_at = PAGED ? b * a.v_stride[0] + n * a.v_stride[2] + col0 : 0;
+  auto load = [&](int head0) {
 #pragma unroll
-        for (int i = 0; i < 8; i += 4) {
-          const float4 x = *reinterpret_cast<const float4*>(row + 8 * u + i);
-          const float4 y = *reinterpret_cast<const float4*>(row + a.R / 2 + 8 * u + i);
-          c[i] = x.x, c[i + 1] = x.y, c[i + 2] = x.z, c[i + 3] = x.w;
-          s[i] = y.x, s[i + 1] = y.y, s[i + 2] = y.z, s[i + 3] = y.w;
-        }
-      }
+    for (int i = 0; i < kHeads; ++i) {
+      const int h = head0 + i * lanes;
+      on[i] = here && h < heads;
+      x[i] = y[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (!on[i] || (PAGED && n >= fresh)) continue;           // behind the sequence's last row: zeros
+      const uint16_t* src = h < a.H ? a.q + (q_at + h * a.q_stride[1])
+                            : !PAGED || h < a.H + a.Hkv ? a.k + (k_at + (h - a.H) * a.k_stride[1])
+                                                        : a.v + (v_at + (h - a.H - a.Hkv) * a.v_stride[1]);
+      x[i] = __ldcs(reinterpret_cast<const uint4*>(src));
+      if (pair) y[i] = __ldcs(reinterpret_cast<const uint4*>(src + half));
+    }
+  };
+  load(threadIdx.y);
+
+  // position, and where the token's key and value go
+  bool real = true, write = true;                              // real: not a row behind its sequence's last
+  long long p = n, page_row = 0;                               // page_row: of key head 0 in the pool
+  if (PAGED) {
+    const AppendSlot at = append_slot(a.seq_lens[b], fresh, a.N, n,
+                                      a.block_table + static_cast<long long>(b) * a.table_width, a.table_width,
+                                      a.page_shift, a.num_pages);
+    real = at.real;
+    p = at.position;
+    write = at.page >= 0;
+    page_row = page_row_of(at.page, a.Hkv, 0, p, a.page_shift);
+    if (here && real && !write) atomicCAS(a.status, 0, kStatusIndex);
+  } else if (a.positions != nullptr) {
+    p = a.positions[static_cast<long long>(b) * a.position_stride + n];
+  }
+  // A position outside the table is reported and left unturned.
+  bool turn = here && u < rot_units && real;
+  if (turn && (p < 0 || p >= a.table_rows)) {
+    atomicCAS(a.status, 0, kStatusIndex);
+    turn = false;
+  }
+  // c: cosine of column j's pair; s: factor of column j's partner (first of a pair: minus the sine)
+  float c[8], s[8];
+  if (turn) {
+    const float* row = a.table + p * a.R;
+    if (kWide) {
+      load8(row + 8 * u, c);
+      load8(row + half + 8 * u, s);
+    } else if (LAYOUT == kInterleaved) {
+      const float4 cc = *reinterpret_cast<const float4*>(row + 4 * u);
+      const float4 ss = *reinterpret_cast<const float4*>(row + half + 4 * u);
+      c[0] = c[1] = cc.x, c[2] = c[3] = cc.y, c[4] = c[5] = cc.z, c[6] = c[7] = cc.w;
+      s[0] = -ss.x, s[1] = ss.x, s[2] = -ss.y, s[3] = ss.y, s[4] = -ss.z, s[5] = ss.z, s[6] = -ss.w, s[7] = ss.w;
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int col = 8 * u + i;
-        const int pair = LAYOUT == kInterleaved ? col >> 1 : (col < a.R / 2 ? col : col - a.R / 2);
-        const bool in = turn && col < a.R;
-        c[i] = in ? row[pair] : 1.f;
-        s[i] = in ? row[a.R / 2 + pair] : 0.f;
-        // the sign of the partner's term: minus for the first of a pair
-        if (LAYOUT == kInterleaved ? (i & 1) == 0 : col < a.R / 2) s[i] = -s[i];
+      for (int j = 0; j < 8; ++j) {
+        const int col = 8 * u + j;
+        const int at = LAYOUT == kInterleavedOdd ? col >> 1 : (col < half ? col : col - half);
+        const bool in = col < a.R;
+        c[j] = in ? row[at] : 1.f;
+        s[j] = in ? row[half + at] : 0.f;
+        if (LAYOUT == kInterleavedOdd ? (j & 1) == 0 : col < half) s[j] = -s[j];
       }
     }
     if (a.inverse) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = -s[i];
-    }
-    const int col0 = LAYOUT == kHalfWide ? (u < rot_units ? 8 * u : 8 * u + a.R / 2) : 8 * u;
-
-    uint4 x[HEADS], y[HEADS];
-    const uint16_t* src[HEADS];
-    uint16_t* dst[HEADS];
-    bool on[HEADS], value[HEADS];
-#pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-      const int h = head0 + i * head_lanes;
-      on[i] = h < heads;
-      value[i] = PAGED && h >= a.H + a.Hkv;
-      src[i] = nullptr;
-      dst[i] = nullptr;
-      if (!on[i]) continue;
-      if (h < a.H) {
-        src[i] = a.q + b * a.q_stride[0] + h * a.q_stride[1] + n * a.q_stride[2];
-        dst[i] = a.q_out + ((static_cast<long long>(b) * a.H + h) * a.N + n) * a.D;
-      } else {
-        const int hk = value[i] ? h - a.H - a.Hkv : h - a.H;
-        const long long* st = value[i] ? a.v_stride : a.k_stride;
-        src[i] = (value[i] ? a.v : a.k) + b * st[0] + hk * st[1] + n * st[2];
-        if (PAGED) {
-          on[i] = real && write;
-          dst[i] = (value[i] ? a.v_out : a.k_out) + (page_row + (static_cast<long long>(hk) << a.page_shift)) * a.D;
-        } else {
-          dst[i] = a.k_out + ((static_cast<long long>(b) * a.Hkv + hk) * a.N + n) * a.D;
-        }
-      }
-      if (!on[i]) continue;
-      src[i] += col0;
-      dst[i] += col0;
-      x[i] = *reinterpret_cast<const uint4*>(src[i]);
-      if (LAYOUT == kHalfWide && u < rot_units) y[i] = *reinterpret_cast<const uint4*>(src[i] + a.R / 2);
-    }
-#pragma unroll
-    for (int i = 0; i < HEADS; ++i) {
-      if (!on[i]) continue;
-      if (PAGED && !real) {                                    // only query heads get here
-        *reinterpret_cast<uint4*>(dst[i]) = make_uint4(0u, 0u, 0u, 0u);
-        if (LAYOUT == kHalfWide && u < rot_units) *reinterpret_cast<uint4*>(dst[i] + a.R / 2) = make_uint4(0u, 0u, 0u, 0u);
-        continue;
-      }
-      if (!turn || value[i]) {
-        *reinterpret_cast<uint4*>(dst[i]) = x[i];
-        if (LAYOUT == kHalfWide && u < rot_units) *reinterpret_cast<uint4*>(dst[i] + a.R / 2) = y[i];
-        continue;
-      }
-      float f[8], g[8], o[8];
-      unpack8<F16>(x[i], f);
-      if (LAYOUT == kHalfWide) {
-        unpack8<F16>(y[i], g);
-        float o2[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          o[j] = f[j] * c[j] - g[j] * s[j];
-          o2[j] = g[j] * c[j] + f[j] * s[j];
-        }
-        *reinterpret_cast<uint4*>(dst[i] + a.R / 2) = pack8<F16>(o2);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float partner = 0.f;
-          if (LAYOUT == kInterleaved) {
-            partner = f[j ^ 1];
-          } else {
-            const int col = col0 + j;
-            if (col < a.R) partner = load16<F16>(src[i] + j + (col < a.R / 2 ? a.R / 2 : -(a.R / 2)));
-          }
-          o[j] = f[j] * c[j] + partner * s[j];
-        }
-      }
-      *reinterpret_cast<uint4*>(dst[i]) = pack8<F16>(o);
+      for (int j = 0; j < 8; ++j) s[j] = -s[j];
     }
   }
-}
 
-template <int LAYOUT, bool F16, bool PAGED, int HEADS>
-cudaError_t launch_heads(const RotaryLaunch& a, cudaStream_t stream) {
-  const int heads = a.H + a.Hkv * (PAGED ? 2 : 1);
-  const int units = LAYOUT == kHalfWide ? a.R / 16 + (a.D - a.R) / 8 : a.D / 8;
-  const int head_lanes = (heads + HEADS - 1) / HEADS;
-  const long long width = static_cast<long long>(head_lanes) * units;
-  int per_block = static_cast<int>(kThreads / width);
-  if (per_block < 1) per_block = 1;
-  const long long tokens = static_cast<long long>(a.B) * a.N;
-  rotary_kernel<LAYOUT, F16, PAGED, HEADS>
-      <<<static_cast<unsigned>((tokens + per_block - 1) / per_block), kThreads, 0, stream>>>(a, per_block, units, head_lanes);
-  return cudaGetLastError();
+  for (int head0 = threadIdx.y;;) {
+    const uint16_t* mine = nullptr;                            // kHalfOdd: this thread's rows in shared memory
+    if (LAYOUT == kHalfOdd) {
+      uint4* rows = staged + (threadIdx.z * lanes + threadIdx.y) * kHeads * blockDim.x;
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i)
+        if (on[i]) rows[i * blockDim.x + u] = x[i];
+      mine = reinterpret_cast<const uint16_t*>(rows);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kHeads; ++i) {
+      const int h = head0 + i * lanes;
+      if (!on[i]) continue;
+      const bool is_q = h < a.H, is_v = PAGED && h >= a.H + a.Hkv;
+      uint16_t* dst;
+      if (is_q) {
+        dst = a.q_out + ((static_cast<long long>(b) * a.H + h) * a.N + n) * a.D + col0;
+      } else if (PAGED) {
+        if (!real || !write) continue;
+        const int hk = is_v ? h - a.H - a.Hkv : h - a.H;
+        dst = (is_v ? a.v_out : a.k_out) + (page_row + (static_cast<long long>(hk) << a.page_shift)) * a.D + col0;
+      } else {
+        dst = a.k_out + ((static_cast<long long>(b) * a.Hkv + (h - a.H)) * a.N + n) * a.D + col0;
+      }
+      uint4 lo = x[i], hi = y[i];
+      if (turn && !is_v) {
+        float f[8], o[8];
+        unpack8<F16>(x[i], f);
+        if (kWide) {
+          float g[8], o2[8];
+          unpack8<F16>(y[i], g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            o[j] = f[j] * c[j] - g[j] * s[j];
+            o2[j] = g[j] * c[j] + f[j] * s[j];
+          }
+          hi = pack8<F16>(o2);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float partner = f[j ^ 1];
+            if (LAYOUT == kHalfOdd) {
+              const int col = col0 + j;
+              // columns past R have s = 0, and their own value is one that is there
+              const int other = col >= a.R ? col : (col < half ? col + half : col - half);
+              partner = unpack16_lo<F16>(mine[i * blockDim.x * 8 + other]);
+              if (col >= a.R) partner = 0.f;
+            }
+            if (LAYOUT == kInterleavedOdd && col0 + j >= a.R) partner = 0.f;
+            o[j] = f[j] * c[j] + partner * s[j];
+          }
+        }
+        lo = pack8<F16>(o);
+      }
+      *reinterpret_cast<uint4*>(dst) = lo;
+      if (pair) *reinterpret_cast<uint4*>(dst + half) = hi;
+    }
+    head0 += kHeads * lanes;
+    // the same for every thread of the block: the first head lane decides
+    if (head0 - static_cast<int>(threadIdx.y) >= heads) break;
+    if (LAYOUT == kHalfOdd) __syncthreads();                   // the rows are read
+    load(head0);
+  }
 }
 
 template <int LAYOUT, bool F16, bool PAGED>
 cudaError_t launch_layout(const RotaryLaunch& a, cudaStream_t stream) {
-  return launch_heads<LAYOUT, F16, PAGED, 1>(a, stream);
+  const int heads = a.H + a.Hkv * (PAGED ? 2 : 1);
+  const int units = LAYOUT == kHalfWide ? a.R / 16 + (a.D - a.R) / 8 : a.D / 8;
+  int lanes = (heads + kHeads - 1) / kHeads;
+  if (lanes > kThreads / units) lanes = kThreads / units;
+  const long long tokens = static_cast<long long>(a.B) * a.N;
+  int per_block = kThreads / (units * lanes);
+  if (per_block > 64) per_block = 64;                          // the grid's z limit of a block
+  if (per_block > tokens) per_block = static_cast<int>(tokens);
+  const dim3 block(units, lanes, per_block);
+  const size_t smem = LAYOUT == kHalfOdd ? sizeof(uint4) * units * lanes * per_block * kHeads : 0;
+  rotary_kernel<LAYOUT, F16, PAGED><<<static_cast<unsigned>((tokens + per_block - 1) / per_block), block, smem, stream>>>(a);
+  return cudaGetLastError();
 }
 
 template <bool F16, bool PAGED>
 cudaError_t launch_type(const RotaryLaunch& a, cudaStream_t stream) {
-  if (a.R == 0 || a.interleaved) return launch_layout<kInterleaved, F16, PAGED>(a, stream);
+  if (a.R == 0) return launch_layout<kInterleaved, F16, PAGED>(a, stream);
+  if (a.interleaved)
+    return a.R % 8 == 0 ? launch_layout<kInterleaved, F16, PAGED>(a, stream)
+                        : launch_layout<kInterleavedOdd, F16, PAGED>(a, stream);
   return a.R % 16 == 0 ? launch_layout<kHalfWide, F16, PAGED>(a, stream) : launch_layout<kHalfOdd, F16, PAGED>(a, stream);
 }
 
