@@ -27,6 +27,7 @@
 //   dK(i), dQ(i), dV(i+1), dP^T(i+1), S^T(i+2)
 // and of the element-wise warps: dS(i), P(i+1), drain dQ(i); so the tensor pipe works on
 // dK/dQ while P(i+1) is computed and on dV(i+1) while dQ(i) is drained.
+#include <climits>
 #include <cstdint>
 #include <math_constants.h>
 #include <type_traits>
@@ -76,9 +77,12 @@ struct FusedSmem {
 
 // The score-modified instances (MOD, see the forward) walk, per key tile of one key-value head, the
 // query tiles that meet it in each of the H / Hkv query heads that share that head, one head after
-// the other: dK_j and dV_j stay in tensor memory over all of them.  With CAP the score gradient
-// carries the factor 1 - tanh^2 = 4 sigma (1 - sigma), folded into a second 16-bit copy of P
-// (`pw`) before dS is formed, so dS is rounded as often as without a cap.
+// the other: dK_j and dV_j stay in tensor memory over all of them.  Where that leaves few and long
+// work items, two CTAs (a cluster) take half of the heads each and join their halves at the end.  With CAP the score gradient
+// carries the factor 1 - tanh^2, folded into the copy of P that dS is formed from.  That copy (`pw`)
+// is kept apart from the operand of dV: as fp16 times 2^12 where the operand is bf16, so that dS
+// gets P to 11 bits and loses only its own rounding (scores that weigh below 2^-26 keep fewer bits,
+// and matter less).
 template <int D, bool CAUSAL, bool F16, bool MOD, bool CAP, bool ALIBI>
 __global__ void __launch_bounds__(kThreads, 1)
     bwd_fused_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -101,9 +105,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   // Work item: key tile kt of head bh (causal: tile 0, which meets every query tile, first).
-  const WorkItem wi = grouped_order(static_cast<int>(blockIdx.x), BH, nkt, hg);
-  const int bh = wi.bh, kt = wi.tile;     // MOD: bh is a key-value head
-  const int kv0 = kt * 128;
+  const int pair = MOD ? static_cast<int>(cluster_size()) : 1;   // CTAs that share a work item: 1 or 2
+  const int rank = MOD ? static_cast<int>(cluster_rank()) : 0;
+  const WorkItem wi = grouped_order(static_cast<int>(blockIdx.x) / pair, BH, nkt, hg);
+  const int bh = wi.bh;                   // MOD: a key-value head
+  int kt = wi.tile;
+  int kv0 = kt * 128;
   int it0 = CAUSAL ? kt : 0;              // first query tile
   int nq = nkt - it0;                     // query tiles of one query head that meet this key tile
   int n = nq;                             // query tiles visited (>= 1; MOD: >= 0, over all heads)
@@ -111,16 +118,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   if constexpr (MOD) {
     const int group = mods.H / mods.Hkv;
     batch = bh / mods.Hkv;
-    qh0 = batch * mods.H + (bh - batch * mods.Hkv) * group;
+    qh0 = batch * mods.H + (bh - batch * mods.Hkv) * group + rank * (group / pair);
     if (mods.plan != nullptr) {
-      const int4 tl = mask_plan_view(mods.plan, BH / mods.Hkv, N).tiles[batch * nkt + kt];
+      const MaskPlan plan = mask_plan_view(mods.plan, BH / mods.Hkv, N);
+      kt = plan.order[static_cast<size_t>(batch) * nkt + kt].x;
+      kv0 = kt * 128;
+      const int4 tl = plan.tiles[static_cast<size_t>(batch) * nkt + kt];
       it0 = tl.z;
       nq = tl.w - tl.z;
     } else {
       it0 = mods.causal ? kt : 0;
       nq = nkt - it0;
     }
-    n = nq * group;
+    n = nq * (group / pair);
   }
 
   if (threadIdx.x == 0) {
@@ -309,19 +319,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool key_oob = key >= N;                       // padding rows of the last key tile
     const bool tail = __any_sync(0xffffffffu, key_oob);  // warp-uniform
     const float scale_log2 = scale * kLog2e;
-    // CAP: 2 cap log2e (times sigma), -cap log2e, and -2 scale log2e / cap (sigma's exponent)
-    const float x_scale = CAP ? 2.f * mods.softcap * kLog2e : scale_log2;
-    const float cap_add = CAP ? -mods.softcap * kLog2e : 0.f;
-    const float sig_scale = CAP ? -2.f * scale_log2 / mods.softcap : 0.f;
+    const float x_scale = CAP ? mods.softcap * kLog2e : scale_log2;   // CAP: of tanh(s / cap)
+    const float cap_in = CAP ? scale / mods.softcap : 0.f;
     const float2 sl2 = make_float2(x_scale, x_scale);
+    const int2* rows = nullptr;                          // MOD: the plan's intervals of this batch element
+    if (MOD && mods.plan != nullptr) rows = mask_plan_view(mods.plan, BH / mods.Hkv, N).rows + static_cast<size_t>(batch) * Npad;
     int pqt = it0, pqh = 0;                              // MOD: query tile and head (within the group) of p_tile's next step
     int dqt = it0, dqh = 0;                              // and of drain's
     // Row r of the dS^T tile (box g/2 holds queries [64(g/2), 64(g/2)+64)); chunk c of a row sits at c ^ (r % 8).
     uint8_t* ds_row = smem + L::kOffDS + (g >> 1) * L::kDSBox + r * 128;
     const int sw = r & 7;
     float* dq_head = ws_dq + static_cast<size_t>(qh0) * Npad * D;
-    uint32_t pw[CAP ? 16 : 1];                           // CAP: packed P^T (1 - tanh^2)
     uint32_t pk[16];                                     // packed P^T of the current tile
+    constexpr bool kWide = MOD && !F16;                  // pw holds fp16 of 2^12 P
+    constexpr bool kOwnW = CAP || kWide;                 // pw differs from pk
+    constexpr float kWScale = kWide ? 4096.f : 1.f, kWBack = 1.f / kWScale;
+    uint32_t pw[kOwnW ? 16 : 1];                         // packed P^T (1 - tanh^2) for dS
     // dQ of the previous query tile (this thread: query row r, D/4 columns), held in registers
     // from its drain out of tensor memory until its 16-byte reductions are issued, a few at a
     // time, between the next tile's dS^T and P^T arithmetic.  Each SM can send only about
@@ -342,6 +355,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // P^T[r][c] = exp2(s * scale * log2e + nl_c), zero where key > query or key >= N; with
     // `reds`, issues the held reductions kReds/2 .. kReds-1 along the way.
     auto p_tile = [&](int i, bool reds) -> bool {
+      int mod_qc0 = 0;
+      int2 iv = make_int2(0, INT_MAX);                   // MOD: the keys that query mod_qc0 + lane sees
+      float slope2 = 0.f;
+      if constexpr (MOD) {
+        // read before the wait for the scores; padding queries (P = 0 by their statistics) bound nothing
+        mod_qc0 = pqt * 128 + 32 * g;
+        const int row = mod_qc0 + lane;
+        if (row < N) iv = mods.plan != nullptr ? rows[row] : make_int2(0, mods.causal ? row + 1 : N);
+        if (ALIBI) slope2 = mods.slopes[qh0 - batch * mods.H + pqh] * kLog2e;
+        if (++pqt == it0 + nq) {
+          pqt = it0;
+          ++pqh;
+        }
+      }
       const int s = i % L::kStages;
       bool ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarQFull + s), (i / L::kStages) & 1, abort_flag));
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarS), i & 1, abort_flag));
@@ -349,23 +376,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       FA_CONVERGED(status);                              // warp-collective TMEM loads follow
       tc_fence_after();
       const float4* st = reinterpret_cast<const float4*>(smem + L::kOffStat + s * L::kStatBytes) + 8 * g;
-      const int qc0 = (MOD ? pqt : it0 + i) * 128 + 32 * g;   // query of this thread's column 0
+      const int qc0 = MOD ? mod_qc0 : (it0 + i) * 128 + 32 * g;   // query of this thread's column 0
       bool edge = tail || (CAUSAL && __any_sync(0xffffffffu, qc0 < key + 32));   // warp-uniform
-      const int2* rows = nullptr;                        // MOD: the intervals of this thread's 32 queries
-      float slope2 = 0.f;
+      uint32_t seen = 0xffffffffu;                       // MOD: bit c: this key is seen by query qc0 + c
       if constexpr (MOD) {
-        if (mods.plan != nullptr) {
-          const MaskPlan plan = mask_plan_view(mods.plan, BH / mods.Hkv, N);
-          rows = plan.rows + static_cast<size_t>(batch) * Npad + qc0;
-          const int2 all = plan.groups[(static_cast<size_t>(batch) * Npad + qc0) / 32];
-          edge = all.x > kv0 || all.y < kv0 + 128;
-        } else {
-          edge = tail || (mods.causal && qc0 + 1 < kv0 + 128);
-        }
-        if (ALIBI) slope2 = mods.slopes[qh0 - batch * mods.H + pqh] * kLog2e;
-        if (++pqt == it0 + nq) {
-          pqt = it0;
-          ++pqh;
+        edge = !__all_sync(0xffffffffu, iv.x <= kv0 && iv.y >= kv0 + 128);
+        if (edge) {
+          // lane c: which of the warp's keys query c sees; turned around, which queries see this key
+          const int w0 = key - lane;
+          const int from = min(max(iv.x - w0, 0), 32), to = min(max(iv.y - w0, 0), 32);
+          uint32_t word = to > from ? (0xffffffffu >> (32 - (to - from))) << from : 0u;
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) {
+            const uint32_t low = d == 16 ? 0x0000ffffu : d == 8 ? 0x00ff00ffu : d == 4 ? 0x0f0f0f0fu : d == 2 ? 0x33333333u : 0x55555555u;
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, word, d);
+            word = (lane & d) ? (word & ~low) | ((other >> d) & low) : (word & low) | ((other << d) & ~low);
+          }
+          seen = word;
         }
       }
       // two halves of 16 columns (one TMEM load each), to keep the held dQ values in registers
@@ -376,6 +403,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld16(tb + kColS + 32 * g + 16 * hf, sr);
           tmem_ld_wait();
           reg_fence(sr);
+          if constexpr (CAP) {                           // scores -> tanh(s / cap), as in the forward
+            float most = 0.f;
+#pragma unroll
+            for (int c = 0; c < 16; c += 2) most = fmax3_abs(most, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+            if (__all_sync(0xffffffffu, most <= mods.poly_limit)) {
+#pragma unroll
+              for (int c = 0; c < 16; c += 2) {
+                const float2 sv = make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+                const float2 th = __fmul2_rn(sv, quartic2(sv, mods.poly));
+                sr[c] = __float_as_uint(th.x);
+                sr[c + 1] = __float_as_uint(th.y);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) sr[c] = __float_as_uint(tanh_mufu(__uint_as_float(sr[c]) * cap_in));
+            }
+          }
 #pragma unroll
           for (int c4 = 4 * hf; c4 < 4 * hf + 4; ++c4) {
             const float4 nl = st[c4];
@@ -385,11 +429,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float2 nlp = h ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y);
               float2 sv = make_float2(__uint_as_float(sr[cl]), __uint_as_float(sr[cl + 1]));
               float2 add = nlp;
-              if constexpr (CAP) {
-                sv.x = rcp_approx(1.f + ex2_approx(sv.x * sig_scale));
-                sv.y = rcp_approx(1.f + ex2_approx(sv.y * sig_scale));
-                add = __fadd2_rn(add, make_float2(cap_add, cap_add));
-              }
               if constexpr (ALIBI) {
                 const float d0 = static_cast<float>(qc0 + c - key);
                 add.x = fmaf(-slope2, fabsf(d0), add.x);
@@ -398,22 +437,18 @@ __global__ void __launch_bounds__(kThreads, 1)
               float2 p = exp2_pair(__ffma2_rn(sv, sl2, add), poly_pair(c2));
               if (decltype(masked)::value) {
                 if constexpr (MOD) {
-                  int4 iv;                               // (lo, hi) of queries c and c + 1
-                  if (rows != nullptr) iv = *reinterpret_cast<const int4*>(rows + c);
-                  else iv = mods.causal ? make_int4(0, qc0 + c + 1, 0, qc0 + c + 2) : make_int4(0, N, 0, N);
-                  if (key < iv.x || key >= iv.y || key_oob) p.x = 0.f;
-                  if (key < iv.z || key >= iv.w || key_oob) p.y = 0.f;
+                  if (!((seen >> c) & 1u)) p.x = 0.f;
+                  if (!((seen >> (c + 1)) & 1u)) p.y = 0.f;
                 } else {
                   if (key_oob || (CAUSAL && key > qc0 + c)) p.x = 0.f;
                   if (key_oob || (CAUSAL && key > qc0 + c + 1)) p.y = 0.f;
                 }
               }
               pk[c2] = pack16<F16>(p.x, p.y);
-              if constexpr (CAP) {
-                // 1 - tanh^2 = 4 sigma (1 - sigma)
-                const float2 w = __fmul2_rn(p, __fmul2_rn(__fmul2_rn(sv, make_float2(4.f, 4.f)),
-                                                          __ffma2_rn(sv, make_float2(-1.f, -1.f), make_float2(1.f, 1.f))));
-                pw[c2] = pack16<F16>(w.x, w.y);
+              if constexpr (kOwnW) {
+                float2 w = __fmul2_rn(p, make_float2(kWScale, kWScale));
+                if constexpr (CAP) w = __fmul2_rn(w, __ffma2_rn(sv, make_float2(-sv.x, -sv.y), make_float2(1.f, 1.f)));
+                pw[c2] = kWide ? pack16<true>(w.x, w.y) : pack16<F16>(w.x, w.y);
               }
             }
             if (reds && kReds == 8 && (c4 & 1)) red_held(4 + (c4 >> 1));         // reductions 4..7
@@ -452,9 +487,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int c2 = 2 * c4 + h, c = 2 * c2;
             const float2 dlp = h ? make_float2(dl.z, dl.w) : make_float2(dl.x, dl.y);
             const float2 dpv = make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1]));
-            const uint32_t pp = CAP ? pw[(8 * hf + c2) & (CAP ? 15 : 0)] : pk[8 * hf + c2];
-            const float2 ds = __fmul2_rn(make_float2(unpack16_lo<F16>(pp), unpack16_hi<F16>(pp)),
-                                         __ffma2_rn(dlp, make_float2(-1.f, -1.f), dpv));
+            const uint32_t pp = kOwnW ? pw[(8 * hf + c2) & (kOwnW ? 15 : 0)] : pk[8 * hf + c2];
+            constexpr bool kHalfP = F16 || kWide;
+            const float2 ds = __fmul2_rn(make_float2(unpack16_lo<kHalfP>(pp), unpack16_hi<kHalfP>(pp)),
+                                         __ffma2_rn(dlp, make_float2(-kWBack, -kWBack),
+                                                    kWide ? __fmul2_rn(dpv, make_float2(kWBack, kWBack)) : dpv));
             dsk[c2] = pack16<F16>(ds.x, ds.y);
           }
         }
@@ -528,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const int wrow = (warp & 3) * 32;
       const int nbox = T::kNBox;                          // 1 (D=64) or 2 (D=128)
-      if (g < 2 * nbox) {
+      if (pair == 1 && g < 2 * nbox) {
         const bool is_dv = g < nbox;
         const int box = is_dv ? g : g - nbox;
         uint8_t* stage = smem + (is_dv ? L::kOffV : L::kOffK);
@@ -541,6 +578,61 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         store_warp_box<D>(is_dv ? &tmdV : &tmdK, sb + (is_dv ? L::kOffV : L::kOffK), box, wrow, kv0, bh, lane, N);
       }
+    }
+  }
+
+  if constexpr (MOD) {
+    if (pair == 2) {
+      // Each CTA holds dK and dV of half of the group's query heads: CTA 0 finishes dV, CTA 1 dK,
+      // each with the other's fp32 half out of its shared memory ([16-byte chunk][row], over the K
+      // and V tiles).  Both barriers are reached by every thread, in a failing CTA too.
+      constexpr int kC = D / 4;                           // columns a thread
+      const int g = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;
+      const uint32_t tb = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+      auto load = [&](uint32_t col, uint32_t (&o)[kC]) {
+        if (n > 0) {
+#pragma unroll
+          for (int c = 0; c < kC; c += 16)
+            tmem_ld16(tb + col + g * kC + c, reinterpret_cast<uint32_t(&)[16]>(o[c]));
+          tmem_ld_wait();
+          reg_fence(o);
+        } else {                                          // no query sees these keys
+#pragma unroll
+          for (int c = 0; c < kC; ++c) o[c] = 0u;
+        }
+      };
+      __syncthreads();
+      tc_fence_after();
+      if (warp >= 4) {
+        FA_CONVERGED(status);
+        uint32_t o[kC];
+        load(rank == 0 ? kColDK : kColDV, o);
+#pragma unroll
+        for (int c = 0; c < kC; c += 4)
+          *reinterpret_cast<uint4*>(smem + ((g * kC + c) / 4 * 128 + r) * 16) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+      }
+      cluster_sync();
+      if (warp >= 4) {
+        FA_CONVERGED(status);
+        uint32_t o[kC];
+        load(rank == 0 ? kColDV : kColDK, o);
+        const float mul = rank == 0 ? 1.f : scale;
+#pragma unroll
+        for (int c = 0; c < kC; c += 8) {
+          const float4 x = ld_cluster_f32x4(sb + ((g * kC + c) / 4 * 128 + r) * 16, rank ^ 1);
+          const float4 y = ld_cluster_f32x4(sb + ((g * kC + c + 4) / 4 * 128 + r) * 16, rank ^ 1);
+          auto sum = [&](int e, float p) { return (__uint_as_float(o[c + e]) + p) * mul; };
+          const int col = g * kC + c;                     // chunk col / 8 % 8 of box col / 64
+          *reinterpret_cast<uint4*>(smem + L::kOffQ + (col >> 6) * T::kBox + r * 128 + ((((col >> 3) & 7) ^ (r & 7)) << 4)) =
+              make_uint4(pack16<F16>(sum(0, x.x), sum(1, x.y)), pack16<F16>(sum(2, x.z), sum(3, x.w)),
+                         pack16<F16>(sum(4, y.x), sum(5, y.y)), pack16<F16>(sum(6, y.z), sum(7, y.w)));
+        }
+        fence_async_smem();
+      }
+      __syncthreads();
+      if (warp >= 4 && g < T::kNBox && *abort_flag == 0)
+        store_warp_box<D>(rank == 0 ? &tmdV : &tmdK, sb + L::kOffQ, g, (warp & 3) * 32, kv0, bh, lane, N);
+      cluster_sync();
     }
   }
 
@@ -592,6 +684,17 @@ __global__ void __launch_bounds__(256) bwd_dq_finish_kernel(const float* __restr
   }
 }
 
+// Whether pairs of CTAs share the work items of a score-modified call: where the items are few, the
+// longest of them (all query tiles of all heads of a group) decide.  Measured, one CTA an item
+// against a pair: D = 128, H / Hkv = 4: N = 4096 causal 64 items 434 / 238 us, packed documents of
+// N = 16384 256 items 626 / 491 us, 256 items (B2 H32 N4096) 1075 / 811 us, 1024 items 1582 / 1587 us;
+// D = 64, whose items are shorter against the joining: 16 items 58 / 40 us, 256 items 201 / 215 us,
+// 1024 items 692 / 756 us.
+template <int D>
+bool pair_items(long long items, const ScoreMods& m, int num_sms) {
+  return m.H / m.Hkv % 2 == 0 && items < (D == 128 ? 4LL : 1LL) * num_sms;
+}
+
 template <int D, bool CAUSAL, bool F16, bool MOD, bool CAP, bool ALIBI>
 cudaError_t fused_impl(const BwdLaunch& a, const ScoreMods& m, cudaStream_t stream) {
   using L = FusedSmem<D>;
@@ -599,10 +702,23 @@ cudaError_t fused_impl(const BwdLaunch& a, const ScoreMods& m, cudaStream_t stre
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   const int nkt = (a.N + 127) / 128;
-  const int BH = MOD ? a.BH / m.H * m.Hkv : a.BH;     // one CTA per key tile of a key-value head
-  kern<<<static_cast<unsigned>(nkt) * BH, kThreads, L::kBytes, stream>>>(
-      a.tmQ, a.tmK, a.tmV, a.tmdO, a.tmdK, a.tmdV, a.ws_nl, a.ws_delta, a.ws_dq, a.N, a.Npad, BH, nkt, a.hg,
-      a.scale, a.status, m);
+  const int BH = MOD ? a.BH / m.H * m.Hkv : a.BH;     // one CTA (or pair) per key tile of a key-value head
+  const long long items = static_cast<long long>(nkt) * BH;
+  const unsigned pair = MOD && pair_items<D>(items, m, a.num_sms) ? 2 : 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(items) * pair);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = pair;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = pair > 1 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, kern, a.tmQ, a.tmK, a.tmV, a.tmdO, a.tmdK, a.tmdV, a.ws_nl, a.ws_delta, a.ws_dq, a.N,
+                         a.Npad, BH, nkt, a.hg, a.scale, a.status, m);
+  if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
 
@@ -643,7 +759,11 @@ cudaError_t launch_bwd_fused(const BwdLaunch& a, cudaStream_t stream) {
   return a.f16 ? fused_typed<true>(a, stream) : fused_typed<false>(a, stream);
 }
 
-cudaError_t launch_bwd_fused_mod(const BwdLaunch& a, const ScoreMods& m, cudaStream_t stream) {
+cudaError_t launch_bwd_fused_mod(const BwdLaunch& a, const ScoreMods& mods, cudaStream_t stream) {
+  ScoreMods m = mods;
+  if (m.softcap != 0.f)
+    set_cap_poly(&m, static_cast<double>(a.scale) / m.softcap, 1.0, {kTanhC0, kTanhC1, kTanhC2, kTanhC3, kTanhC4},
+                 kTanhPolyLimit);
   if (a.DK == 64) return a.f16 ? fused_mod_typed<64, true>(a, m, stream) : fused_mod_typed<64, false>(a, m, stream);
   if (a.DK == 128) return a.f16 ? fused_mod_typed<128, true>(a, m, stream) : fused_mod_typed<128, false>(a, m, stream);
   return cudaErrorInvalidValue;

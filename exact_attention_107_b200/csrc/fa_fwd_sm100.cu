@@ -32,6 +32,7 @@
 // result is unchanged while most O rescales (a TMEM round trip) are skipped; the
 // un-normalised probabilities stay below 2^8.
 #include <cstdint>
+#include <type_traits>
 #include <math_constants.h>
 
 #include "fa_internal.h"
@@ -82,10 +83,11 @@ struct FwdSmem {
 // The score-modified instances (MOD) run the same pipeline with, per batch element, query rows
 // that see an interval of keys each (a mask plan, or full / causal), key-value heads shared by
 // H / Hkv query heads, and optionally
-//   CAP    x = cap tanh(s / cap) for s = scale q.k.  tanh(z) = 2 sigma(2z) - 1, so the score
-//          registers are replaced by sigma = 1 / (1 + 2^(-c s)) and the softmax runs on
-//          2 cap log2e sigma, its constant -cap joining only lse.  sigma's error, about 2^-22, is
-//          an error of cap 2^-21 in x; the hardware tanh's 2^-11 would be one of cap / 2000.
+//   CAP    x = cap tanh(s / cap), s = scale q.k.  The score registers are replaced by the tanh and
+//          the softmax runs on cap log2e tanh.  Two MUFU operations a score for an accurate tanh
+//          next to the exponential's one made the MUFU unit the limit (B1 H8 N16384 D128 causal:
+//          1176 us against 483 without a cap); scores up to 0.75 cap, as nearly all are, take a
+//          polynomial on the FMA pipe instead (a warp's choice for its 32 rows of a tile).
 //   ALIBI  x -= slope_h |i - j|, in fp32 on the scores before the row maximum.
 // Rows that see nothing get O = 0 and lse = -inf.
 template <int D, bool CAUSAL, bool F16, bool MOD, bool CAP, bool ALIBI>
@@ -119,6 +121,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   int kv_bh = bh, batch = 0;
   if constexpr (MOD) {
     batch = bh / mods.H;
+    if (mods.plan != nullptr)
+      qblk = mask_plan_view(mods.plan, BH / mods.H, N).order[static_cast<size_t>(batch) * nkv_all + (nqb - 1 - qblk)].y;
     kv_bh = batch * mods.Hkv + (bh - batch * mods.H) / (mods.H / mods.Hkv);
   }
 #pragma unroll
@@ -128,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     nkv[t] = (q0[t] >= N) ? 0 : (causal ? min(nkv_all, q0[t] / kBN + 1) : nkv_all);
     if constexpr (MOD) {
       if (mods.plan != nullptr && q0[t] < N) {
-        const int4 tl = mask_plan_view(mods.plan, BH / mods.H, N).tiles[batch * nkv_all + q0[t] / kBM];
+        const int4 tl = mask_plan_view(mods.plan, BH / mods.H, N).tiles[static_cast<size_t>(batch) * nkv_all + q0[t] / kBM];
         ka[t] = tl.x;
         nkv[t] = tl.y - tl.x;
       }
@@ -301,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float m = -CUDART_INF_F, l = 0.f;
     // MOD: the keys [lo, hi) that this row sees (none for rows past N).
     int lo = 0, hi = 0;
-    float slope2 = 0.f, sig_scale = 0.f, lse_add = 0.f;   // slope * log2e; -2 scale / cap * log2e; -cap
+    float slope2 = 0.f, cap_in = 0.f;                     // slope * log2e; scale / cap
     float softmax_scale = scale_log2;                     // multiplies the score registers in the exponent
     if constexpr (MOD) {
       if (qrow < N) {
@@ -313,13 +317,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (CAP) {
-        sig_scale = -2.f * scale_log2 / mods.softcap;
-        softmax_scale = 2.f * mods.softcap * kLog2e;
-        lse_add = -mods.softcap;
+        cap_in = scale_log2 * kLn2 / mods.softcap;
+        softmax_scale = mods.softcap * kLog2e;
       }
       if (ALIBI) slope2 = mods.slopes[bh - batch * mods.H] * kLog2e;
     }
-    const float x_scale = ALIBI ? 1.f : softmax_scale;    // ALIBI scales before the bias is subtracted
     bool ok = true;
     for (int j = 0; j < nkv[t]; ++j) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarSFull + t), j & 1, abort_flag));
@@ -338,30 +340,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       reg_fence(sr[3]);
       const int kv0 = MOD ? (j0 + ka[t] + j) * kBN : j * kBN;
       const bool diag = CAUSAL && (kv0 + kBN - 1 > q0[t]);
+      // The score registers stay raw (masked ones -inf): the maximum is found on them, and the
+      // exponentials' arguments are formed on the fly.
+      bool small = true;                                  // CAP: every score of the warp's is in the polynomial's range
       if constexpr (CAP) {
+        float most[2] = {0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < kBN; ++c)
-          sr[c >> 5][c & 31] = __float_as_uint(
-              rcp_approx(1.f + ex2_approx(__uint_as_float(sr[c >> 5][c & 31]) * sig_scale)));
-      }
-      if constexpr (ALIBI) {
-        // x - slope |i - j|: linear in the column where every key of the tile lies on one side of
-        // the warp's rows, element by element around the diagonal.
-        const int wrow0 = qrow - lane;
-        const float d0 = static_cast<float>(qrow - kv0);
-        if (kv0 + kBN - 1 <= wrow0 || kv0 >= wrow0 + 31) {
-          const float s2 = kv0 >= wrow0 + 31 ? -slope2 : slope2;
-          const float base = -s2 * d0;
-#pragma unroll
-          for (int c = 0; c < kBN; ++c)
-            sr[c >> 5][c & 31] = __float_as_uint(
-                fmaf(__uint_as_float(sr[c >> 5][c & 31]), softmax_scale, fmaf(s2, static_cast<float>(c), base)));
-        } else {
-#pragma unroll
-          for (int c = 0; c < kBN; ++c)
-            sr[c >> 5][c & 31] = __float_as_uint(fmaf(__uint_as_float(sr[c >> 5][c & 31]), softmax_scale,
-                                                      -slope2 * fabsf(d0 - static_cast<float>(c))));
-        }
+        for (int c = 0; c < kBN; c += 2)
+          most[(c >> 1) & 1] = fmax3_abs(most[(c >> 1) & 1], __uint_as_float(sr[c >> 5][c & 31]),
+                                         __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
+        small = __all_sync(0xffffffffu, fmaxf(most[0], most[1]) <= mods.poly_limit);
       }
       if constexpr (MOD) {
         if (!__all_sync(0xffffffffu, lo <= kv0 && hi >= kv0 + kBN)) {
@@ -377,12 +365,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kBN; ++c)
           if (c > lim) sr[c >> 5][c & 31] = 0xff800000u;                  // -inf
       }
-      float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+      // ALIBI: every key of the tile lies on one side of the warp's rows
+      const bool one_side = kv0 + kBN - 1 <= qrow - lane || kv0 >= qrow - lane + 31;
+      // cap tanh(x / cap), of one score and log2e-scaled; -inf stays
+      auto capped = [&](float x) { return x == -CUDART_INF_F ? x : softmax_scale * tanh_mufu(x * cap_in); };
+      float m_tile;
+      if constexpr (ALIBI) {
+        // The reference needs no exact maximum, only one that is not far above it: of eight columns
+        // to one side of the warp's rows the largest score and the least bias, at most 7 |slope| log2e
+        // too high.  Slopes for which that is more than the rescaling threshold, and tiles around the
+        // diagonal, take column by column.
+        const float d0 = static_cast<float>(qrow - kv0);
+        float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+        if (one_side && fabsf(slope2) * 7.f <= kRescaleThreshold) {
+          const float s2 = kv0 >= qrow - lane + 31 ? -slope2 : slope2;   // the bias grows by s2 a column
+          const float base = fmaf(-s2, d0, s2 > 0.f ? 7.f * s2 : 0.f);
 #pragma unroll
-      for (int c = 0; c < kBN; c += 2)
-        mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(sr[c >> 5][c & 31]),
-                                 __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
-      const float m_tile = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * x_scale;
+          for (int c = 0; c < kBN; c += 8) {
+            const int q = c >> 5, e = c & 31;
+            float v = fmax3(__uint_as_float(sr[q][e]), __uint_as_float(sr[q][e + 1]), __uint_as_float(sr[q][e + 2]));
+            v = fmax3(v, __uint_as_float(sr[q][e + 3]), __uint_as_float(sr[q][e + 4]));
+            v = fmax3(v, __uint_as_float(sr[q][e + 5]), fmaxf(__uint_as_float(sr[q][e + 6]), __uint_as_float(sr[q][e + 7])));
+            const float bias = fmaf(s2, static_cast<float>(c), base);
+            if constexpr (CAP) {
+              const float2 v2 = make_float2(v, v);
+              v = (small ? v * quartic2(v2, mods.poly).x : capped(v)) + bias;
+            } else {
+              v = fmaf(v, softmax_scale, bias);
+            }
+            top[(c >> 3) & 1] = fmaxf(top[(c >> 3) & 1], v);
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kBN; c += 2) {
+            float2 v = make_float2(__uint_as_float(sr[c >> 5][c & 31]), __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
+            if constexpr (CAP) v = small ? __fmul2_rn(v, quartic2(v, mods.poly)) : make_float2(capped(v.x), capped(v.y));
+            else v = make_float2(v.x * softmax_scale, v.y * softmax_scale);
+            const float e = d0 - static_cast<float>(c);
+            top[0] = fmaxf(top[0], fmaf(-slope2, fabsf(e), v.x));
+            top[1] = fmaxf(top[1], fmaf(-slope2, fabsf(e - 1.f), v.y));
+          }
+        }
+        m_tile = fmaxf(top[0], top[1]);
+      } else {
+        float mx[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+        for (int c = 0; c < kBN; c += 2)
+          mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(sr[c >> 5][c & 31]),
+                                   __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
+        const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        m_tile = CAP ? capped(most) : most * scale_log2;
+      }
       const float m_new = fmaxf(m, m_tile);
       const bool need = m_new > m + kRescaleThreshold;                     // always true at j == 0
       const float m_use = need ? m_new : m;
@@ -393,50 +426,96 @@ __global__ void __launch_bounds__(kThreads, 1)
       // announced on its own barrier, so the P V products of the first half overlap the
       // exponentials of the second.
       float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      const float2 sl2 = make_float2(x_scale, x_scale), neg2 = make_float2(neg, neg);
+      // arg(c, s): the exponents of columns 2c and 2c + 1, whose scores are s
+      auto exponentials = [&](auto arg) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        // P of keys [64h, 64h+64) as packed pairs, stored 16 pairs at a time (nothing reads
-        // them before this half's barrier arrival below), to keep the registers for S.
+        for (int h = 0; h < 2; ++h) {
+          // P of keys [64h, 64h+64) as packed pairs, stored 16 (CAP: 8) pairs at a time (nothing reads
+          // them before this half's barrier arrival below), to keep the registers for S.
+          constexpr int kPk = CAP ? 8 : 16;
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
-          uint32_t pk[16];
+          for (int hh = 0; hh < 32 / kPk; ++hh) {
+            uint32_t pk[kPk];
 #pragma unroll
-          for (int c2 = 0; c2 < 16; ++c2) {
-            const int c = 32 * h + 16 * hh + c2;           // pair index: columns 2c, 2c + 1
-            const float2 sv = make_float2(__uint_as_float(sr[(2 * c) >> 5][(2 * c) & 31]),
-                                          __uint_as_float(sr[(2 * c + 1) >> 5][(2 * c + 1) & 31]));
-            const float2 p = exp2_pair(__ffma2_rn(sv, sl2, neg2), poly_pair<D>(c));
-            sum[c & 1] = __fadd2_rn(sum[c & 1], p);
-            pk[c2] = pack16<F16>(p.x, p.y);
-          }
-          tmem_st16(tS + 32 * h + 16 * hh, pk);
-        }
-        if (h == 0 && j > 0 && __any_sync(0xffffffffu, need)) {
-          FA_CONVERGED(status);
-          // Rescale O_t before any of this step's P V products lands in it (after the
-          // first half's exponentials, whose scores no longer occupy registers).  O_t was
-          // finished by the PV MMAs of step j-1: the commit that announced S_t(j) also
-          // covers every earlier MMA of this thread, including those.
-#pragma unroll
-          for (int cc = 0; cc < D / 32; ++cc) {
-            uint32_t o[32];
-            tmem_ld32(tO + cc * 32, o);
-            tmem_ld_wait();
-            reg_fence(o);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
-                                          make_float2(alpha, alpha));
-              o[i] = __float_as_uint(v.x);
-              o[i + 1] = __float_as_uint(v.y);
+            for (int c2 = 0; c2 < kPk; ++c2) {
+              const int c = 32 * h + kPk * hh + c2;          // pair index: columns 2c, 2c + 1
+              const float2 sv = make_float2(__uint_as_float(sr[(2 * c) >> 5][(2 * c) & 31]),
+                                            __uint_as_float(sr[(2 * c + 1) >> 5][(2 * c + 1) & 31]));
+              const float2 p = exp2_pair(arg(c, sv), poly_pair<D>(c));
+              sum[c & 1] = __fadd2_rn(sum[c & 1], p);
+              pk[c2] = pack16<F16>(p.x, p.y);
             }
-            tmem_st32(tO + cc * 32, o);
+            if constexpr (CAP) tmem_st8(tS + 32 * h + kPk * hh, pk);
+            else tmem_st16(tS + 32 * h + kPk * hh, pk);
           }
+          if (h == 0 && j > 0 && __any_sync(0xffffffffu, need)) {
+            FA_CONVERGED(status);
+            // Rescale O_t before any of this step's P V products lands in it (after the
+            // first half's exponentials, whose scores no longer occupy registers).  O_t was
+            // finished by the PV MMAs of step j-1: the commit that announced S_t(j) also
+            // covers every earlier MMA of this thread, including those.
+#pragma unroll
+            for (int cc = 0; cc < D / 32; ++cc) {
+              uint32_t o[32];
+              tmem_ld32(tO + cc * 32, o);
+              tmem_ld_wait();
+              reg_fence(o);
+#pragma unroll
+              for (int i = 0; i < 32; i += 2) {
+                const float2 v = __fmul2_rn(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])),
+                                            make_float2(alpha, alpha));
+                o[i] = __float_as_uint(v.x);
+                o[i + 1] = __float_as_uint(v.y);
+              }
+              tmem_st32(tO + cc * 32, o);
+            }
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bar(L::kBarPFull + 2 * h + t));
         }
-        tmem_st_wait();
-        tc_fence_before();
-        mbar_arrive(bar(L::kBarPFull + 2 * h + t));
+      };
+      const float2 sl2 = make_float2(softmax_scale, softmax_scale), neg2 = make_float2(neg, neg);
+      if constexpr (!CAP && !ALIBI) {
+        exponentials([&](int, float2 sv) { return __ffma2_rn(sv, sl2, neg2); });
+      } else {
+        // softmax_scale tanh(score) (CAP: by the polynomial or the MUFU unit) or score, plus `add`
+        auto exponent = [&](auto poly, float2 sv, float2 add) {
+          if constexpr (!CAP) return __ffma2_rn(sv, sl2, add);
+          if constexpr (decltype(poly)::value) return __ffma2_rn(sv, quartic2(sv, mods.poly), add);
+          const float2 z = __fmul2_rn(sv, make_float2(cap_in, cap_in));
+          return __ffma2_rn(make_float2(sv.x == -CUDART_INF_F ? sv.x : tanh_mufu(z.x),
+                                        sv.y == -CUDART_INF_F ? sv.y : tanh_mufu(z.y)), sl2, add);
+        };
+        auto with_bias = [&](auto poly) {
+          if constexpr (!ALIBI) {
+            exponentials([&](int, float2 sv) { return exponent(poly, sv, neg2); });
+          } else {
+            // bias - m: to one side of the rows linear in the column (16 columns by additions from a
+            // product), |i - j| around the diagonal
+            const float d0 = static_cast<float>(qrow - kv0);
+            if (one_side) {
+              const float s2 = kv0 >= qrow - lane + 31 ? -slope2 : slope2;
+              float2 bias = make_float2(0.f, 0.f);
+              exponentials([&](int c, float2 sv) {
+                if (c % 8 == 0) {
+                  const float b0 = fmaf(s2, static_cast<float>(2 * c) - d0, neg);
+                  bias = make_float2(b0, b0 + s2);
+                } else {
+                  bias = __fadd2_rn(bias, make_float2(2.f * s2, 2.f * s2));
+                }
+                return exponent(poly, sv, bias);
+              });
+            } else {
+              exponentials([&](int c, float2 sv) {
+                const float e = d0 - static_cast<float>(2 * c);
+                return exponent(poly, sv, make_float2(fmaf(-slope2, fabsf(e), neg), fmaf(-slope2, fabsf(e - 1.f), neg)));
+              });
+            }
+          }
+        };
+        if (!CAP || small) with_bias(std::true_type{});
+        else with_bias(std::false_type{});
       }
       l = l * alpha + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
       m = m_use;
@@ -485,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bulk_wait_read0();
       }
       if (qrow < N && FA_BOUNDS(static_cast<size_t>(bh) < static_cast<size_t>(BH), status))
-        lse[static_cast<size_t>(bh) * N + qrow] = m * kLn2 + logf(l) + (CAP ? lse_add : 0.f);
+        lse[static_cast<size_t>(bh) * N + qrow] = m * kLn2 + logf(l);
     }
   }
 
@@ -542,7 +621,11 @@ cudaError_t launch_fwd_16(const FwdLaunch& a, cudaStream_t stream) {
   return a.f16 ? launch_typed<true>(a, stream) : launch_typed<false>(a, stream);
 }
 
-cudaError_t launch_fwd_mod(const FwdLaunch& a, const ScoreMods& m, cudaStream_t stream) {
+cudaError_t launch_fwd_mod(const FwdLaunch& a, const ScoreMods& mods, cudaStream_t stream) {
+  ScoreMods m = mods;
+  if (m.softcap != 0.f)
+    set_cap_poly(&m, static_cast<double>(a.scale) / m.softcap, static_cast<double>(m.softcap) * kLog2e,
+                 {kTanhC0, kTanhC1, kTanhC2, kTanhC3, kTanhC4}, kTanhPolyLimit);
   if (a.D <= 64) return a.f16 ? launch_mod_typed<64, true>(a, m, stream) : launch_mod_typed<64, false>(a, m, stream);
   return a.f16 ? launch_mod_typed<128, true>(a, m, stream) : launch_mod_typed<128, false>(a, m, stream);
 }

@@ -34,29 +34,44 @@ struct ScoreMods {
   float softcap;        // 0: none
   int H, Hkv;           // query and key-value heads per batch element
   int causal;           // without a plan: 1 = key j visible to query i iff j <= i
+  // softcap: out tanh(in s) = s (poly[0] + poly[1] s^2 + ...) for |s| <= poly_limit, set by
+  // set_cap_poly; poly_limit < 0 where the coefficients leave the floats' normal range.
+  float poly[5], poly_limit;
 };
+// The polynomial of out tanh(in s) (coefficients of tanh: kTanhC0 .. kTanhC4).
+inline void set_cap_poly(ScoreMods* m, double in, double out, const float (&tanh_c)[5], float limit) {
+  m->poly_limit = static_cast<float>(limit / in);
+  double power = in * out;
+  for (int j = 0; j < 5; ++j, power *= in * in) {
+    const double c = tanh_c[j] * power;
+    m->poly[j] = static_cast<float>(c);
+    if (!(c * c > 1e-72 && c * c < 1e72) || !(in > 1e-15)) m->poly_limit = -1.f;
+  }
+}
 
 // Layout of a mask plan for B batch elements of N rows (int32, 16-byte aligned), Npad = N
 // rounded up to a multiple of 128, nt = Npad / 128:
-//   rows    [B][Npad]     int2  (lo, hi): row i sees the keys lo <= j < hi (padding rows: 0, 0)
-//   groups  [B][Npad/32]  int2  (largest lo, smallest hi) of 32 rows: keys in between are seen by all
-//   tiles   [B][nt]       int4  (first, end) key tile that query tile t meets, (first, end) query
-//                               tile that key tile t meets; first = end where there is none
+//   rows    [B][Npad]  int2  (lo, hi): row i sees the keys lo <= j < hi (padding rows: 0, 0)
+//   tiles   [B][nt]    int4  (first, end) key tile that query tile t meets, (first, end) query tile
+//                            that key tile t meets; first = end where there is none
+//   order   [B][nt]    int2  x: the key tiles, those that meet most query tiles first; y: the same
+//                            for blocks of two query tiles ((nt + 1) / 2 of them): long work items
+//                            started last leave the other SMs idle at the end
 struct MaskPlan {
   const int2* rows;
-  const int2* groups;
   const int4* tiles;
+  const int2* order;
 };
 __host__ __device__ inline size_t mask_plan_ints(size_t B, size_t N) {
   const size_t npad = (N + 127) / 128 * 128;
-  return B * (2 * npad + 2 * (npad / 32) + 4 * (npad / 128));
+  return B * (2 * npad + (4 + 2) * (npad / 128));
 }
 __host__ __device__ inline MaskPlan mask_plan_view(const int* plan, int B, int N) {
   const size_t npad = (static_cast<size_t>(N) + 127) / 128 * 128;
   MaskPlan v;
   v.rows = reinterpret_cast<const int2*>(plan);
-  v.groups = v.rows + B * npad;
-  v.tiles = reinterpret_cast<const int4*>(v.groups + B * (npad / 32));
+  v.tiles = reinterpret_cast<const int4*>(v.rows + B * npad);
+  v.order = reinterpret_cast<const int2*>(v.tiles + B * (npad / 128));
   return v;
 }
 // Builds a plan from optional document ids (B, N) and prefix lengths (B) (fa_mod.cu).

@@ -10,7 +10,7 @@
 // One CTA per batch element.  The rows' run starts become one bit each (a ballot per warp, ids read
 // once, coalesced); a scan over the N / 32 words gives each word the last start before it and the
 // first one after it, so a row finds its run with a bit scan in its own word.  Bound by latency,
-// not by its 4 bytes read and 8.6 written a row: 1024 threads of one SM walk all N rows.
+// not by its 4 bytes read and 8.2 written a row: 1024 threads of one SM walk all N rows.
 #include <climits>
 #include <cstdint>
 
@@ -61,7 +61,7 @@ __global__ void __launch_bounds__(kThreads) mask_plan_kernel(int* __restrict__ p
   int* first_after = last_before + nw;                              // [nw] first run start in the words after
   const MaskPlan v = mask_plan_view(plan, B, N);
   int2* rows = const_cast<int2*>(v.rows) + static_cast<size_t>(b) * npad;
-  int2* groups = const_cast<int2*>(v.groups) + static_cast<size_t>(b) * (npad / 32);
+  int2* order = const_cast<int2*>(v.order) + static_cast<size_t>(b) * nt;
   int4* tiles = const_cast<int4*>(v.tiles) + static_cast<size_t>(b) * nt;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int* doc = documents != nullptr ? documents + static_cast<size_t>(b) * N : nullptr;
@@ -143,20 +143,20 @@ __global__ void __launch_bounds__(kThreads) mask_plan_kernel(int* __restrict__ p
       if (hi <= lo) lo = hi = 0;
     }
     rows[i] = make_int2(lo, hi);
-    // rows past N constrain nothing
-    const int max_lo = __reduce_max_sync(0xffffffffu, i < N ? lo : 0);
-    const int min_hi = __reduce_min_sync(0xffffffffu, i < N ? hi : INT_MAX);
     const int min_lo = __reduce_min_sync(0xffffffffu, hi > lo ? lo : INT_MAX);
     const int max_hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) {
-      groups[w] = make_int2(max_lo, min_hi);
       atomicMin(&tile_lo[w >> 2], min_lo);
       atomicMax(&tile_hi[w >> 2], max_hi);
     }
   }
   __syncthreads();
   // Key tile kt is met by the query tiles whose range holds it; every mask here makes them
-  // neighbours, up to tiles of rows that see nothing.
+  // neighbours, up to tiles of rows that see nothing.  Work of a query block: its two tiles' ranges.
+  int* q_work = scan_buf + 32;       // [nt] over the run starts, which are read
+  int* k_work = q_work + nt;         // [nt]
+  const int nqb = (nt + 1) / 2;
+  __syncthreads();
   for (int t = threadIdx.x; t < nt; t += kThreads) {
     int4 r = make_int4(0, 0, 0, 0);
     if (tile_hi[t] > 0) {
@@ -175,6 +175,25 @@ __global__ void __launch_bounds__(kThreads) mask_plan_kernel(int* __restrict__ p
       r.w = q_end;
     }
     tiles[t] = r;
+    k_work[t] = r.w - r.z;
+    q_work[t] = r.y - r.x;
+  }
+  __syncthreads();
+  int* block_work = k_work + nt;     // [nqb]
+  for (int t = threadIdx.x; t < nqb; t += kThreads) block_work[t] = q_work[2 * t] + (2 * t + 1 < nt ? q_work[2 * t + 1] : 0);
+  __syncthreads();
+  // place of each item: the items with more work, and those with as much before it
+  for (int t = threadIdx.x; t < nt; t += kThreads) {
+    const int kw = k_work[t], qw = t < nqb ? block_work[t] : 0;
+    int k_at = 0, q_at = 0;
+    for (int o = 0; o < nt; ++o) k_at += k_work[o] > kw || (k_work[o] == kw && o < t);
+    order[k_at].x = t;
+    if (t < nqb) {
+      for (int o = 0; o < nqb; ++o) q_at += block_work[o] > qw || (block_work[o] == qw && o < t);
+      order[q_at].y = t;
+    } else {
+      order[t].y = t;                // not a block: never read
+    }
   }
 }
 
@@ -183,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) mask_plan_kernel(int* __restrict__ p
 cudaError_t launch_mask_plan(int* plan, const int* documents, const int* prefix, int B, int N, int causal, int window,
                              cudaStream_t stream) {
   const size_t nt = (static_cast<size_t>(N) + 127) / 128;
-  const size_t bytes = (2 * nt + 32 + (documents != nullptr ? 3 * 4 * nt : 0)) * sizeof(int);
+  const size_t bytes = (2 * nt + 32 + (documents != nullptr ? 3 * 4 * nt : 3 * nt)) * sizeof(int);
   cudaError_t e = cudaFuncSetAttribute(mask_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(bytes));
   if (e != cudaSuccess) return e;

@@ -282,6 +282,33 @@ __device__ __forceinline__ void reg_fence(uint32_t (&r)[N]) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// ----------------------------------------------------------------------------- clusters
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Barrier of every thread of the cluster; what was written to shared memory before is visible after.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// 16 bytes of another CTA's shared memory, at the address that `addr` has in this one.
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr, uint32_t rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
 // ----------------------------------------------------------------------------- descriptors
 // Shared-memory matrix descriptor, 128-byte swizzle (tcgen05 "version 1" format):
 // start address, leading- and stride-dimension byte offsets (all >> 4).
@@ -348,6 +375,31 @@ __device__ __forceinline__ float2 exp2_poly2(float2 x) {
   const float2 scale = make_float2(__int_as_float(__float_as_int(t.x) << 23), __int_as_float(__float_as_int(t.y) << 23));
   return __fmul2_rn(p, scale);
 }
+// tanh(z) = z (C0 + C1 z^2 + ... + C4 z^8) for |z| <= kTanhPolyLimit: the quartic in z^2 that
+// minimises the maximum relative error (Remez exchange; derived by gen_tanh_poly.py in this
+// directory).  Max relative error 7e-7.
+constexpr float kTanhPolyLimit = 0.75f;
+constexpr float kTanhC0 = 0.99999946355819702f;   // 0x3f7ffff7
+constexpr float kTanhC1 = -0.33328250050544739f;  // 0xbeaaa401
+constexpr float kTanhC2 = 0.13258983194828033f;   // 0x3e07c5a1
+constexpr float kTanhC3 = -0.05005630105733871f;  // 0xbd4d07d6
+constexpr float kTanhC4 = 0.01292963232845068f;   // 0x3c53d6cf
+// x times the quartic in x^2 with coefficients c, for a pair, on the FMA pipe: with c_j = out C_j
+// in^(2j + 1) this is out tanh(in x).  `quartic2` leaves the last product to the caller.  x = -inf
+// gives -inf (the last coefficient is positive).
+__device__ __forceinline__ float2 quartic2(float2 x, const float (&c)[5]) {
+  const float2 u = __fmul2_rn(x, x);
+  float2 p = __ffma2_rn(u, make_float2(c[4], c[4]), make_float2(c[3], c[3]));
+  p = __ffma2_rn(p, u, make_float2(c[2], c[2]));
+  p = __ffma2_rn(p, u, make_float2(c[1], c[1]));
+  return __ffma2_rn(p, u, make_float2(c[0], c[0]));
+}
+// tanh for any z on the MUFU unit, 2 / (1 + 2^(-2 log2e z)) - 1.  Absolute error about 2^-21: two
+// MUFU operations of relative error 2^-22 (tanh.approx's 2^-11 would be an error of cap / 2000 in a
+// capped score).
+__device__ __forceinline__ float tanh_mufu(float z) {
+  return fmaf(2.f, rcp_approx(1.f + ex2_approx(z * -2.88539008177792681472f)), -1.f);
+}
 // 2^x for a pair: on the FMA pipe when `poly`, else two MUFU ex2.approx.
 __device__ __forceinline__ float2 exp2_pair(float2 x, bool poly) {
   return poly ? exp2_poly2(x) : make_float2(ex2_approx(x.x), ex2_approx(x.y));
@@ -381,6 +433,12 @@ __device__ __forceinline__ float unpack16_hi(uint32_t x) {
   return __uint_as_float(x & 0xffff0000u);
 }
 
+// Three-input maximum of a and the magnitudes of b and c (one instruction on sm_100).
+__device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
 // Three-input maximum (one instruction on sm_100).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;

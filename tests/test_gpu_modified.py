@@ -39,8 +39,9 @@ def documents(B, N, kind):
 
 def mask_args(kind, B, N):
     """(arguments of attention_mask or None, causal argument of the call, dense visibility)"""
-    if kind in ("full", "causal"):
-        return None, kind == "causal", ref.visible(B, N, causal=kind == "causal")
+    if kind in ("full", "causal", "hot", "steep", "steep-full"):
+        causal = kind in ("causal", "hot", "steep")
+        return None, causal, ref.visible(B, N, causal=causal)
     if kind.startswith("doc"):
         _, which, *rest = kind.split("-")
         a = dict(documents=documents(B, N, which), causal="full" not in rest)
@@ -75,6 +76,13 @@ CASES = [
     (1, 2, 1, 200, 32, "windowN-full", 5.0, False, "fp16"),
     (1, 8, 1, 256, 128, "causal", 30.0, False, "bf16"),
     (1, 8, 2, 385, 64, "full", 0.0, False, "fp16"),
+    # more work items than SMs: one CTA for all heads of a group
+    (5, 20, 10, 300, 64, "doc-padded", 0.0, False, "bf16"),
+    # scores far beyond the cap (the other way to its tanh), and steep slopes
+    (1, 4, 2, 300, 128, "hot", 5.0, False, "bf16"),
+    (1, 4, 2, 300, 64, "hot", 3.0, True, "fp16"),
+    (1, 2, 2, 400, 64, "steep", 0.0, True, "fp16"),
+    (1, 2, 1, 300, 128, "steep-full", 20.0, True, "bf16"),
 ]
 
 
@@ -90,9 +98,11 @@ def slopes_of(H, alibi):
 
 @pytest.mark.parametrize("B,H,Hkv,N,D,kind,cap,alibi,dtype", CASES)
 def test_forward_and_gradients(B, H, Hkv, N, D, kind, cap, alibi, dtype):
-    q, k, v, do = inputs(B, H, Hkv, N, D, dtype, N + D)
+    q, k, v, do = inputs(B, H, Hkv, N, D, dtype, N + D, 8.0 if kind == "hot" else 1.5)
     args, causal, seen = mask_args(kind, B, N)
     slopes, scale = slopes_of(H, alibi), ref.default_scale(D)
+    if kind.startswith("steep"):
+        slopes = torch.tensor([3.0, -0.02])
     want, bound = ref.attention(q, k, v, do, scale, seen, cap, slopes)
     cu = lambda t: None if t is None else t.cuda()
     qd, kd, vd, dod, sd = cu(q), cu(k), cu(v), cu(do), cu(slopes)
@@ -129,7 +139,8 @@ def test_mask_plan_rows(kind, B, N):
     assert torch.equal(dense, seen)
     assert (rows[:, N:] == 0).all()
     nt = npad // 128
-    tiles = plan[2 * B * npad + 2 * B * (npad // 32):].view(B, nt, 4)
+    tiles = plan[2 * B * npad: 2 * B * npad + 4 * B * nt].view(B, nt, 4)
+    order = plan[2 * B * npad + 4 * B * nt:].view(B, nt, 2)
     pad = torch.zeros(B, npad, npad, dtype=torch.bool)
     pad[:, :N, :N] = seen
     blocks = pad.view(B, nt, 128, nt, 128).any(4).any(2)
@@ -137,6 +148,12 @@ def test_mask_plan_rows(kind, B, N):
     by_query = (t >= tiles[:, :, :1]) & (t < tiles[:, :, 1:2])
     by_key = (t >= tiles[:, :, 2:3]) & (t < tiles[:, :, 3:])
     assert not (blocks & ~by_query).any() and not (blocks.transpose(1, 2) & ~by_key).any()
+    # every key tile and query block once, those with most work first
+    work_k, work_q = tiles[..., 3] - tiles[..., 2], tiles[..., 1] - tiles[..., 0]
+    work_q = torch.nn.functional.pad(work_q, (0, nt % 2)).view(B, -1, 2).sum(-1)
+    for items, work in ((order[..., 0], work_k), (order[:, : work_q.shape[1], 1], work_q)):
+        assert torch.equal(items.sort(-1).values, torch.arange(items.shape[1], dtype=torch.int32).expand_as(items))
+        assert (work.gather(1, items.long()).diff(dim=1) <= 0).all()
 
 
 def test_unmodified_call_keeps_its_path():

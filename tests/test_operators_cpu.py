@@ -1,11 +1,14 @@
 """Rotary, paged-cache and score-modified operators without a GPU: refusals of the C ABI and of the
 Python entry points, the page arithmetic, the tables, and the tests' own 64-bit forms."""
 import ctypes
+import importlib.util
 import math
+import re
 import shutil
 import subprocess
 from pathlib import Path
 
+import numpy as np
 import pytest
 import torch
 
@@ -67,9 +70,9 @@ def test_mask_plan_refusals(args, code):
 
 
 def test_mask_plan_size():
-    # per 128 rows: 128 intervals, 4 group summaries and 2 tile ranges of 8 bytes each
-    assert fa.fa_mask_plan_size(1, 1) == 8 * (128 + 4 + 2)
-    assert fa.fa_mask_plan_size(3, 129) == 3 * 2 * 8 * (128 + 4 + 2)
+    # per 128 rows: 128 intervals, 2 tile ranges and an entry of two orders, of 8 bytes each
+    assert fa.fa_mask_plan_size(1, 1) == 8 * (128 + 2 + 1)
+    assert fa.fa_mask_plan_size(3, 129) == 3 * 2 * 8 * (128 + 2 + 1)
     assert fa.fa_mask_plan_size(1, 262144) > 0 and fa.fa_mask_plan_size(1, 262145) == 0
     assert fa.fa_mask_plan_size(0, 5) == 0
 
@@ -229,6 +232,23 @@ def test_rotary_table():
                 dict(scaling="by_parts"), dict(scaling="base", rotary_dim=2), dict(length=0)):
         with pytest.raises(ValueError):
             fa.rotary_table(**{**dict(length=4, rotary_dim=8), **bad})
+
+
+# ----------------------------------------------------------------------------- the capped scores' polynomial
+def test_tanh_polynomial_is_the_fit_and_keeps_its_bound():
+    spec = importlib.util.spec_from_file_location("gen_tanh_poly", CSRC / "gen_tanh_poly.py")
+    g = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(g)
+    text = (CSRC / "sm100_ptx.cuh").read_text()
+    words = re.findall(r"kTanhC\d = -?[0-9.]+f;\s*// 0x([0-9a-f]{8})", text)
+    values = re.findall(r"kTanhC\d = (-?[0-9.]+)f;", text)
+    c = np.array([np.frombuffer(bytes.fromhex(w)[::-1], np.float32)[0] for w in words])
+    assert len(c) == g.TERMS and np.array_equal(c, g.remez_relative().astype(np.float32))
+    assert np.array_equal(c, np.array([float(v) for v in values]).astype(np.float32))
+    assert f"kTanhPolyLimit = {g.LIMIT}f" in text
+    z = np.linspace(1e-7, g.LIMIT, 300001).astype(np.float32)
+    # 5.65e-7 of the fit and a rounding of 2^-24 at each of the last steps
+    assert np.abs(g.eval_f32(z, c).astype(np.float64) / np.tanh(z.astype(np.float64)) - 1).max() <= 5.7e-7 + 4 * 2.0 ** -24
 
 
 # ----------------------------------------------------------------------------- the 64-bit forms
