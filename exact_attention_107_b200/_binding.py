@@ -27,6 +27,7 @@ SYMBOLS = (
 )
 
 _lib = None
+_fast = None        # csrc/fast_call.cpp: the ordinary rotary, paged and score-modified calls in C++
 
 
 class FAError(RuntimeError):
@@ -37,7 +38,7 @@ class FAError(RuntimeError):
 
 def load_library() -> ctypes.CDLL:
     """Loads libfa.so (built in-tree by exact_attention_107_b200.build)."""
-    global _lib
+    global _lib, _fast
     if _lib is not None:
         return _lib
     if not LIB_PATH.exists():
@@ -81,8 +82,26 @@ def load_library() -> ctypes.CDLL:
     lib.fa_paged_workspace_size.argtypes = [i] * 5
     lib.fa_paged_workspace_size.restype = sz
     lib.fa_paged_attention.argtypes = [vp] * 8 + [sz, vp, f] + [i] * 9 + [f, i, vp]
-    _lib = lib
+    try:
+        from . import _fast as fast
+    except ImportError as e:
+        raise RuntimeError("_fast.so is missing or of another torch; build it with "
+                           "`python -m exact_attention_107_b200.build`") from e
+    fast.bind(*(ctypes.cast(getattr(lib, name), vp).value for name in (
+        "fa_rotary", "fa_paged_append", "fa_paged_attention", "fa_paged_workspace_size", "fa_fwd_mod", "fa_bwd_mod",
+        "fa_bwd_workspace_size")))
+    _lib, _fast = lib, fast
     return lib
+
+
+def fast_result(r, where: str):
+    """What a function of _fast returned: its tensors, or None where the Python path has to take the
+    call; a status of the C ABI is raised."""
+    if type(r) is tuple:
+        return r
+    if r is not NotImplemented:
+        _raise(r, where)
+    return None
 
 
 def status_string(status: int) -> str:

@@ -214,7 +214,16 @@ def modified(q, k, mask, softcap, alibi_slopes) -> bool:
         k.dim() == 4 and q.dim() == 4 and k.shape[1] != q.shape[1])
 
 
+def _fits(mask, q):
+    return mask is None or (isinstance(mask, AttentionMask) and q.shape[0] == mask.B and q.shape[2] == mask.N)
+
+
 def modified_forward(q, k, v, scale, causal, stream, mask, softcap, alibi_slopes):
+    if stream is None and base._fast is not None and _fits(mask, q):
+        r = base.fast_result(base._fast.forward(q, k, v, None if mask is None else mask.plan, alibi_slopes, softcap,
+                                                scale, causal), "fa_fwd_mod")
+        if r is not None:
+            return r
     _, _, _, _, _, code, mods = _mod_args(q, k, v, mask, softcap, alibi_slopes, causal)
 
     def call(raw, keep):
@@ -226,6 +235,11 @@ def modified_forward(q, k, v, scale, causal, stream, mask, softcap, alibi_slopes
 
 
 def modified_backward(q, k, v, o, lse, do, scale, causal, stream, workspace, mask, softcap, alibi_slopes):
+    if stream is None and workspace is None and base._fast is not None and _fits(mask, q):
+        r = base.fast_result(base._fast.backward(q, k, v, None if mask is None else mask.plan, alibi_slopes, softcap,
+                                                 scale, causal, o, lse, do), "fa_bwd_mod")
+        if r is not None:
+            return r
     B, H, Hkv, N, D, code, mods = _mod_args(q, k, v, mask, softcap, alibi_slopes, causal)
     _check_grads(q, o, do, lse, B, H, N, D)
     if workspace is not None:

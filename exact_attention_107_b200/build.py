@@ -27,6 +27,8 @@ TIMEOUT_TEST_LIB = PKG / "libfa_timeout_test.so"
 # Debug build: device-side bounds checks of computed indices and warp-convergence checks at
 # the warp-collective tensor-memory phases (a failed check records FA_ERR_DEBUG_CHECK).
 DEBUG_LIB = PKG / "libfa_debug.so"
+# CPython extension with the host side of the small calls (csrc/fast_call.cpp).
+FAST_MODULE = PKG / "_fast.so"
 VARIANTS = {"timeout_test": ["-DFA_WAIT_LIMIT_CYCLES=100"], "debug": ["-DFA_DEBUG_CHECKS"]}
 SOURCES = ["fa_api.cu", "fa_fwd_sm100.cu", "fa_fwd_d256_sm100.cu", "fa_fwd_f32.cu", "fa_bwd_sm100.cu",
            "fa_bwd_d256_sm100.cu", "fa_bwd_fused_sm100.cu", "fa_noalloc.cu", "fa_mask.cu", "fa_rotary.cu",
@@ -42,12 +44,12 @@ def nvcc() -> str:
 
 
 def _deps():
-    return ([CSRC / s for s in SOURCES] + list(CSRC.glob("*.cuh")) + list(CSRC.glob("*.h")) + [INCLUDE / "fa.h"]
+    return ([CSRC / s for s in SOURCES] + [CSRC / "fast_call.cpp"] + list(CSRC.glob("*.cuh")) + list(CSRC.glob("*.h")) + [INCLUDE / "fa.h"]
             + [pathlib.Path(__file__).resolve()])
 
 
 def up_to_date() -> bool:
-    libs = (LIB, TIMEOUT_TEST_LIB, DEBUG_LIB)
+    libs = (LIB, TIMEOUT_TEST_LIB, DEBUG_LIB, FAST_MODULE)
     if not all(lib.exists() for lib in libs):
         return False
     t = min(lib.stat().st_mtime for lib in libs)
@@ -71,6 +73,26 @@ def _compile(src: str, verbose: bool, ptxas_v: bool, variant: str = "") -> pathl
     return obj
 
 
+def _compile_fast(verbose: bool) -> None:
+    import sysconfig
+
+    import torch
+    root = pathlib.Path(torch.__file__).resolve().parent
+    cuda = pathlib.Path(nvcc()).resolve().parents[1] if os.path.exists(nvcc()) else pathlib.Path("/usr/local/cuda")
+    tmp = FAST_MODULE.with_suffix(".so.tmp")
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + str(root / "include"), "-I" + str(root / "include/torch/csrc/api/include"),
+           "-I" + str(cuda / "include"), "-I" + sysconfig.get_paths()["include"], str(CSRC / "fast_call.cpp"),
+           "-o", str(tmp), "-L" + str(root / "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for fast_call.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, FAST_MODULE)
+
+
 def _link(objs, lib: pathlib.Path, verbose: bool) -> None:
     tmp = lib.with_suffix(".so.tmp")
     cmd = [nvcc(), *ARCH, "-shared", "-o", str(tmp), *map(str, objs), "-cudart", "static"]
@@ -91,7 +113,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
     BUILD.mkdir(exist_ok=True)
     jobs = [(s, v) for v in ("", "timeout_test", "debug") for s in SOURCES]
     with cf.ThreadPoolExecutor(max_workers=min(len(jobs), max(4, os.cpu_count() or 4))) as ex:
+        fast = ex.submit(_compile_fast, verbose)
         objs = list(ex.map(lambda j: _compile(j[0], verbose, ptxas_v and not j[1], j[1]), jobs))
+        fast.result()
     n = len(SOURCES)
     _link(objs[:n], LIB, verbose)
     _link(objs[n:2 * n], TIMEOUT_TEST_LIB, verbose)

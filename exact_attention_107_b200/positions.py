@@ -142,6 +142,10 @@ def fa_rotary(q, k, q_out, k_out, table, positions=None, interleaved: bool = Fal
 
 
 def _turn(q, k, table, positions, interleaved, inverse, stream):
+    if stream is None and base._fast is not None:
+        r = base.fast_result(base._fast.rotary(q, k, table, positions, interleaved, inverse), "fa_rotary")
+        if r is not None:
+            return r
     B, H, Hkv, N, D, R, code, dev, middle = _rotary_args(q, k, table, positions)
     tail = (B, H, Hkv, N, D, R, int(interleaved), int(inverse), code)
 
