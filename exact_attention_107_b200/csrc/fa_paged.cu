@@ -70,7 +70,8 @@ struct Smem {
   static constexpr int kOffMax = kOffRows + R * 16;                 // float [2][R][4]: the warps' maxima
   static constexpr int kOffRef = kOffMax + 2 * R * 16;              // float [R] reference maximum, [R] factor
   static constexpr int kOffFlags = kOffRef + 2 * R * 4;             // int [2][4]
-  static constexpr int kOffBar = kOffFlags + 32;
+  static constexpr int kOffSum = kOffFlags + 32;                    // float [R][4]: the warps' sums
+  static constexpr int kOffBar = kOffSum + R * 16;
   static constexpr int kBarKFull = 0, kBarKEmpty = kKSlots, kBarVFull = 2 * kKSlots, kBarVEmpty = kBarVFull + kVSlots;
   static constexpr int kBarQFull = 2 * kSlots, kBarQEmpty = kBarQFull + 2;
   static constexpr int kBarSFull = kBarQEmpty + 2, kBarSEmpty = kBarSFull + 2;
@@ -186,7 +187,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(L::kBarSync), 128);
     *abort_flag = 0;
     fence_mbar_init();
-    ws.splits[blockIdx.x].pieces = 0;
   }
   if (warp == 5) {
     tmem_alloc(smem_u32(tmem_slot), L::kTmemCols);
@@ -197,6 +197,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tmK);
     prefetch_tmap(&tmV);
   }
+
+  // All that the kernel before this one on the stream wrote: lengths, pages, q, and the workspace
+  // that an earlier call's joining kernel still reads.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tid == 0) ws.splits[blockIdx.x].pieces = 0;
 
   // This CTA's piece: the tiles of all sequences before each thread's share of them, then the
   // sequence in which the piece begins.
@@ -483,8 +488,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bar(L::kBarSEmpty + (i & 1)));
         auto X = [&](int n) { return __uint_as_float(x[n]); };
         if (cap) {
+          float most = 0.f;
 #pragma unroll
-          for (int n = 0; n < R; ++n) x[n] = __float_as_uint(cap_out * tanhf(X(n) * cap_in));
+          for (int n = 0; n < R; n += 2) most = fmax3_abs(most, X(n), X(n + 1));
+          if (__all_sync(0xffffffffu, most * cap_in <= kTanhPolyLimit)) {
+            const float tanh_c[5] = {kTanhC0, kTanhC1, kTanhC2, kTanhC3, kTanhC4};
+#pragma unroll
+            for (int n = 0; n < R; n += 2) {
+              const float2 z = __fmul2_rn(make_float2(X(n), X(n + 1)), make_float2(cap_in, cap_in));
+              const float2 th = __fmul2_rn(__fmul2_rn(z, quartic2(z, tanh_c)), make_float2(cap_out, cap_out));
+              x[n] = __float_as_uint(th.x);
+              x[n + 1] = __float_as_uint(th.y);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < R; ++n) x[n] = __float_as_uint(cap_out * tanhf(X(n) * cap_in));
+          }
         } else {
 #pragma unroll
           for (int n = 0; n < R; ++n) x[n] = __float_as_uint(X(n) * scale2);
@@ -618,24 +637,22 @@ __global__ void __launch_bounds__(kThreads, 1)
           l[0] += __shfl_xor_sync(0xffffffffu, l[0], d);
         }
       }
-      if (!(ok = sync())) break;                         // the maxima are read
-      float* wsum = reinterpret_cast<float*>(smem + L::kOffMax);
+      float* wsum = reinterpret_cast<float*>(smem + L::kOffSum);
 #pragma unroll
       for (int n = 0; n < (R > 32 ? 2 : 1); ++n)
         if (R >= 32 || lane % (R >= 32 ? 1 : 32 / R) == 0) wsum[((R >= 32 ? lane * (R / 32) : lane / (R >= 32 ? 1 : 32 / R)) + n) * 4 + warp] = l[n];
       if (!(ok = sync())) break;
       const bool whole = n_tiles == w.s.ntiles;
       const int part = static_cast<int>(blockIdx.x) * 2 + (w.tile == 0 ? 1 : 0);
-      if (tid < R) {
-        const float4 v = *reinterpret_cast<const float4*>(wsum + 4 * tid);
-        const float total_l = (v.x + v.y) + (v.z + v.w), m = ref[tid];
-        ref[R + tid] = !whole ? 1.f : (total_l == 0.f ? 0.f : 1.f / total_l);
-        if (tid < rows_here) {
-          if (whole) a.lse[q_row + tid] = total_l == 0.f ? -CUDART_INF_F : (m + log2f(total_l)) * kLn2;
-          else ws.stats[part * R + tid] = make_float2(m, total_l);
-        }
+      auto row_sum = [&](int n) {
+        const float4 v = *reinterpret_cast<const float4*>(wsum + 4 * n);
+        return (v.x + v.y) + (v.z + v.w);
+      };
+      if (tid < rows_here) {
+        const float total_l = row_sum(tid), m = ref[tid];
+        if (whole) a.lse[q_row + tid] = total_l == 0.f ? -CUDART_INF_F : (m + log2f(total_l)) * kLn2;
+        else ws.stats[part * R + tid] = make_float2(m, total_l);
       }
-      if (!(ok = sync())) break;
       ok = __all_sync(0xffffffffu, mbar_wait(bar(L::kBarPEmpty + (i - 1) % L::kBufs), ((i - 1) / L::kBufs) & 1, abort_flag));
       if (!ok) break;
       FA_CONVERGED(a.status);
@@ -651,18 +668,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_ld_wait();
           reg_fence(o);
           float f[16];
+          if (whole) {
 #pragma unroll
-          for (int e = 0; e < 16; e += 4) {
-            const float4 v = *reinterpret_cast<const float4*>(ref + R + c + e);
-            f[e] = v.x, f[e + 1] = v.y, f[e + 2] = v.z, f[e + 3] = v.w;
+            for (int e = 0; e < 16; ++e) {
+              const float total_l = row_sum(c + e);
+              f[e] = total_l == 0.f ? 0.f : rcp_approx(total_l);     // 2^-23, against a rounding to 16 bits
+            }
           }
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int n = c + e;
             if (n >= rows_here || d >= D) continue;
-            const float value = __uint_as_float(o[e]) * f[e];
-            if (whole) a.o[(q_row + n) * D + d] = static_cast<uint16_t>(pack16<F16>(value, 0.f));
-            else ws.part[(static_cast<size_t>(part) * R + n) * DP + d] = value;
+            if (whole) a.o[(q_row + n) * D + d] = static_cast<uint16_t>(pack16<F16>(__uint_as_float(o[e]) * f[e], 0.f));
+            else ws.part[(static_cast<size_t>(part) * R + n) * DP + d] = __uint_as_float(o[e]);
           }
         }
       }
@@ -764,17 +782,22 @@ cudaError_t launch_impl(const PagedLaunch& a, cudaStream_t stream) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (e != cudaSuccess) return e;
   const int ctas = a.num_sms < kMaxCtas ? a.num_sms : kMaxCtas;
-  kern<<<ctas, kThreads, L::kBytes, stream>>>(tmQ, tmK, tmV, a, geo);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, geo.M < R ? geo.M : R);
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = stream;
+  // Both launched as programmatic dependents: their set-up overlaps the end of the kernel before,
+  // and griddepcontrol.wait holds what depends on it.
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = L::kBytes;
+  cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, kern, tmQ, tmK, tmV, a, geo)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(ctas, geo.M < R ? geo.M : R);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, R, F16>, a, geo);
 }
 
