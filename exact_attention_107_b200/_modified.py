@@ -219,7 +219,7 @@ def _fits(mask, q):
 
 
 def modified_forward(q, k, v, scale, causal, stream, mask, softcap, alibi_slopes):
-    if stream is None and base._fast is not None and _fits(mask, q):
+    if stream is None and base._lib is not None and _fits(mask, q):
         r = base.fast_result(base._fast.forward(q, k, v, None if mask is None else mask.plan, alibi_slopes, softcap,
                                                 scale, causal), "fa_fwd_mod")
         if r is not None:
@@ -235,7 +235,7 @@ def modified_forward(q, k, v, scale, causal, stream, mask, softcap, alibi_slopes
 
 
 def modified_backward(q, k, v, o, lse, do, scale, causal, stream, workspace, mask, softcap, alibi_slopes):
-    if stream is None and workspace is None and base._fast is not None and _fits(mask, q):
+    if stream is None and workspace is None and base._lib is not None and _fits(mask, q):
         r = base.fast_result(base._fast.backward(q, k, v, None if mask is None else mask.plan, alibi_slopes, softcap,
                                                  scale, causal, o, lse, do), "fa_bwd_mod")
         if r is not None:

@@ -32,7 +32,6 @@
 // result is unchanged while most O rescales (a TMEM round trip) are skipped; the
 // un-normalised probabilities stay below 2^8.
 #include <cstdint>
-#include <type_traits>
 #include <math_constants.h>
 
 #include "fa_internal.h"
@@ -342,14 +341,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool diag = CAUSAL && (kv0 + kBN - 1 > q0[t]);
       // The score registers stay raw (masked ones -inf): the maximum is found on them, and the
       // exponentials' arguments are formed on the fly.
-      bool small = true;                                  // CAP: every score of the warp's is in the polynomial's range
       if constexpr (CAP) {
         float most[2] = {0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < kBN; c += 2)
           most[(c >> 1) & 1] = fmax3_abs(most[(c >> 1) & 1], __uint_as_float(sr[c >> 5][c & 31]),
                                          __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
-        small = __all_sync(0xffffffffu, fmaxf(most[0], most[1]) <= mods.poly_limit);
+        if (!__all_sync(0xffffffffu, fmaxf(most[0], most[1]) <= mods.poly_limit)) {
+          // Rare, and so a loop through tensor memory that costs the other tiles no register: scores
+          // beyond the polynomial's range become those for which it gives their tanh.
+          FA_CONVERGED(status);
+          const float out_in = cap_in > 0.f ? 1.f / cap_in : 0.f;
+#pragma unroll 1
+          for (int c = 0; c < kBN; c += 16) {
+            uint32_t x[16];
+            tmem_ld16(tS + c, x);
+            tmem_ld_wait();
+            reg_fence(x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float z = __uint_as_float(x[e]) * cap_in, th = tanh_mufu(z), far = quartic_inverse(fabsf(th)) * out_in;
+              x[e] = mods.poly_limit < 0.f ? __float_as_uint(th)
+                     : fabsf(z) <= kTanhPolyLimit ? x[e] : __float_as_uint(copysignf(far, z));
+            }
+            tmem_st16(tS + c, x);
+          }
+          tmem_st_wait();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, sr[q]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) reg_fence(sr[q]);
+        }
       }
       if constexpr (MOD) {
         if (!__all_sync(0xffffffffu, lo <= kv0 && hi >= kv0 + kBN)) {
@@ -367,8 +390,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // ALIBI: every key of the tile lies on one side of the warp's rows
       const bool one_side = kv0 + kBN - 1 <= qrow - lane || kv0 >= qrow - lane + 31;
-      // cap tanh(x / cap), of one score and log2e-scaled; -inf stays
-      auto capped = [&](float x) { return x == -CUDART_INF_F ? x : softmax_scale * tanh_mufu(x * cap_in); };
+      // log2e cap tanh(score / cap) or log2e score, of a pair
+      auto scaled = [&](float2 v) {
+        if constexpr (CAP) return __fmul2_rn(v, quartic2(v, mods.poly));
+        return make_float2(v.x * softmax_scale, v.y * softmax_scale);
+      };
       float m_tile;
       if constexpr (ALIBI) {
         // The reference needs no exact maximum, only one that is not far above it: of eight columns
@@ -387,20 +413,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             v = fmax3(v, __uint_as_float(sr[q][e + 3]), __uint_as_float(sr[q][e + 4]));
             v = fmax3(v, __uint_as_float(sr[q][e + 5]), fmaxf(__uint_as_float(sr[q][e + 6]), __uint_as_float(sr[q][e + 7])));
             const float bias = fmaf(s2, static_cast<float>(c), base);
-            if constexpr (CAP) {
-              const float2 v2 = make_float2(v, v);
-              v = (small ? v * quartic2(v2, mods.poly).x : capped(v)) + bias;
-            } else {
-              v = fmaf(v, softmax_scale, bias);
-            }
-            top[(c >> 3) & 1] = fmaxf(top[(c >> 3) & 1], v);
+            top[(c >> 3) & 1] = fmaxf(top[(c >> 3) & 1], (CAP ? scaled(make_float2(v, v)).x : v * softmax_scale) + bias);
           }
         } else {
 #pragma unroll
           for (int c = 0; c < kBN; c += 2) {
-            float2 v = make_float2(__uint_as_float(sr[c >> 5][c & 31]), __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
-            if constexpr (CAP) v = small ? __fmul2_rn(v, quartic2(v, mods.poly)) : make_float2(capped(v.x), capped(v.y));
-            else v = make_float2(v.x * softmax_scale, v.y * softmax_scale);
+            const float2 v = scaled(make_float2(__uint_as_float(sr[c >> 5][c & 31]),
+                                                __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31])));
             const float e = d0 - static_cast<float>(c);
             top[0] = fmaxf(top[0], fmaf(-slope2, fabsf(e), v.x));
             top[1] = fmaxf(top[1], fmaf(-slope2, fabsf(e - 1.f), v.y));
@@ -414,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx[(c >> 1) & 3] = fmax3(mx[(c >> 1) & 3], __uint_as_float(sr[c >> 5][c & 31]),
                                    __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31]));
         const float most = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-        m_tile = CAP ? capped(most) : most * scale_log2;
+        m_tile = CAP ? scaled(make_float2(most, most)).x : most * scale_log2;
       }
       const float m_new = fmaxf(m, m_tile);
       const bool need = m_new > m + kRescaleThreshold;                     // always true at j == 0
@@ -479,43 +498,34 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (!CAP && !ALIBI) {
         exponentials([&](int, float2 sv) { return __ffma2_rn(sv, sl2, neg2); });
       } else {
-        // softmax_scale tanh(score) (CAP: by the polynomial or the MUFU unit) or score, plus `add`
-        auto exponent = [&](auto poly, float2 sv, float2 add) {
-          if constexpr (!CAP) return __ffma2_rn(sv, sl2, add);
-          if constexpr (decltype(poly)::value) return __ffma2_rn(sv, quartic2(sv, mods.poly), add);
-          const float2 z = __fmul2_rn(sv, make_float2(cap_in, cap_in));
-          return __ffma2_rn(make_float2(sv.x == -CUDART_INF_F ? sv.x : tanh_mufu(z.x),
-                                        sv.y == -CUDART_INF_F ? sv.y : tanh_mufu(z.y)), sl2, add);
+        auto exponent = [&](float2 sv, float2 add) {
+          return __ffma2_rn(sv, CAP ? quartic2(sv, mods.poly) : sl2, add);
         };
-        auto with_bias = [&](auto poly) {
-          if constexpr (!ALIBI) {
-            exponentials([&](int, float2 sv) { return exponent(poly, sv, neg2); });
+        if constexpr (!ALIBI) {
+          exponentials([&](int, float2 sv) { return exponent(sv, neg2); });
+        } else {
+          // bias - m: to one side of the rows linear in the column (16 columns by additions from a
+          // product), |i - j| around the diagonal
+          const float d0 = static_cast<float>(qrow - kv0);
+          if (one_side) {
+            const float s2 = kv0 >= qrow - lane + 31 ? -slope2 : slope2;
+            float2 bias = make_float2(0.f, 0.f);
+            exponentials([&](int c, float2 sv) {
+              if (c % 8 == 0) {
+                const float b0 = fmaf(s2, static_cast<float>(2 * c) - d0, neg);
+                bias = make_float2(b0, b0 + s2);
+              } else {
+                bias = __fadd2_rn(bias, make_float2(2.f * s2, 2.f * s2));
+              }
+              return exponent(sv, bias);
+            });
           } else {
-            // bias - m: to one side of the rows linear in the column (16 columns by additions from a
-            // product), |i - j| around the diagonal
-            const float d0 = static_cast<float>(qrow - kv0);
-            if (one_side) {
-              const float s2 = kv0 >= qrow - lane + 31 ? -slope2 : slope2;
-              float2 bias = make_float2(0.f, 0.f);
-              exponentials([&](int c, float2 sv) {
-                if (c % 8 == 0) {
-                  const float b0 = fmaf(s2, static_cast<float>(2 * c) - d0, neg);
-                  bias = make_float2(b0, b0 + s2);
-                } else {
-                  bias = __fadd2_rn(bias, make_float2(2.f * s2, 2.f * s2));
-                }
-                return exponent(poly, sv, bias);
-              });
-            } else {
-              exponentials([&](int c, float2 sv) {
-                const float e = d0 - static_cast<float>(2 * c);
-                return exponent(poly, sv, make_float2(fmaf(-slope2, fabsf(e), neg), fmaf(-slope2, fabsf(e - 1.f), neg)));
-              });
-            }
+            exponentials([&](int c, float2 sv) {
+              const float e = d0 - static_cast<float>(2 * c);
+              return exponent(sv, make_float2(fmaf(-slope2, fabsf(e), neg), fmaf(-slope2, fabsf(e - 1.f), neg)));
+            });
           }
-        };
-        if (!CAP || small) with_bias(std::true_type{});
-        else with_bias(std::false_type{});
+        }
       }
       l = l * alpha + ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y));
       m = m_use;

@@ -35,7 +35,8 @@ struct ScoreMods {
   int H, Hkv;           // query and key-value heads per batch element
   int causal;           // without a plan: 1 = key j visible to query i iff j <= i
   // softcap: out tanh(in s) = s (poly[0] + poly[1] s^2 + ...) for |s| <= poly_limit, set by
-  // set_cap_poly; poly_limit < 0 where the coefficients leave the floats' normal range.
+  // set_cap_poly.  poly_limit < 0 (coefficients beyond the floats' normal range): s stands for
+  // tanh(in s) itself.
   float poly[5], poly_limit;
 };
 // The polynomial of out tanh(in s) (coefficients of tanh: kTanhC0 .. kTanhC4).
@@ -45,7 +46,12 @@ inline void set_cap_poly(ScoreMods* m, double in, double out, const float (&tanh
   for (int j = 0; j < 5; ++j, power *= in * in) {
     const double c = tanh_c[j] * power;
     m->poly[j] = static_cast<float>(c);
-    if (!(c * c > 1e-72 && c * c < 1e72) || !(in > 1e-15)) m->poly_limit = -1.f;
+    if (!(c * c > 1e-72 && c * c < 1e72)) m->poly_limit = -1.f;
+  }
+  if (m->poly_limit < 0.f) {
+    m->poly[0] = static_cast<float>(out);
+    m->poly[1] = m->poly[2] = m->poly[3] = 0.f;
+    m->poly[4] = 1e-37f;          // nothing next to poly[0]; -inf still gives -inf, not inf * 0
   }
 }
 

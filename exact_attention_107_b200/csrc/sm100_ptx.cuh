@@ -394,6 +394,19 @@ __device__ __forceinline__ float2 quartic2(float2 x, const float (&c)[5]) {
   p = __ffma2_rn(p, u, make_float2(c[1], c[1]));
   return __ffma2_rn(p, u, make_float2(c[0], c[0]));
 }
+// tanh's quartic beyond its limit: z' with z' (C0 + C1 z'^2 + ...) = t for kTanhPolyLimit's tanh
+// <= t <= 1 (the polynomial rises to 1 at z' = 1.477).  Three Newton steps from a chord leave 2^-22.
+__device__ __forceinline__ float quartic_inverse(float t) {
+  float z = fmaf(t - 0.63514936f, 1.9726f, kTanhPolyLimit);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const float u = z * z;
+    const float p = z * fmaf(fmaf(fmaf(fmaf(kTanhC4, u, kTanhC3), u, kTanhC2), u, kTanhC1), u, kTanhC0);
+    const float d = fmaf(fmaf(fmaf(fmaf(9.f * kTanhC4, u, 7.f * kTanhC3), u, 5.f * kTanhC2), u, 3.f * kTanhC1), u, kTanhC0);
+    z -= __fdividef(p - t, d);
+  }
+  return z;
+}
 // tanh for any z on the MUFU unit, 2 / (1 + 2^(-2 log2e z)) - 1.  Absolute error about 2^-21: two
 // MUFU operations of relative error 2^-22 (tanh.approx's 2^-11 would be an error of cap / 2000 in a
 // capped score).

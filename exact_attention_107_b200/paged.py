@@ -84,7 +84,7 @@ def paged_append(k, v, k_pages, v_pages, block_table, seq_lens, *, new_lens=None
     table is not written and sets the device status (fa_device_status) to FA_ERR_INDEX."""
     if table is None and q is not None:
         raise ValueError("q is turned on the way and needs a table")
-    if stream is None and base._fast is not None:
+    if stream is None and base._lib is not None:
         r = base.fast_result(base._fast.append(k, v, k_pages, v_pages, block_table, seq_lens, new_lens, q, table,
                                                interleaved), "fa_paged_append")
         if r is not None:
@@ -157,7 +157,7 @@ def paged_attention(q, k_pages, v_pages, block_table, seq_lens, scale: float | N
     status (fa_device_status) to FA_ERR_INDEX.  workspace: for callers that keep one, of
     fa_paged_workspace_size bytes; calls that may overlap on the GPU (other streams, captured
     graphs) must not share it."""
-    if stream is None and workspace is None and base._fast is not None:
+    if stream is None and workspace is None and base._lib is not None:
         r = base.fast_result(base._fast.decode(
             q, k_pages, v_pages, block_table, seq_lens, q.shape[-1] ** -0.5 if scale is None else scale, softcap,
             alibi_slopes, window, None), "fa_paged_attention")
