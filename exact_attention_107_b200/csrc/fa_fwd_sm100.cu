@@ -374,6 +374,39 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int q = 0; q < 4; ++q) reg_fence(sr[q]);
         }
       }
+      // ALIBI: the bias is linear in the column where every visible key of the tile lies on one side
+      // of the warp's rows: growing by s2 a column, slope2 to the left and -slope2 to the right.
+      bool one_side = true;
+      float s2 = 0.f;
+      if constexpr (ALIBI) {
+        const bool right = kv0 >= qrow - lane + 31;
+        one_side = right || __all_sync(0xffffffffu, kv0 + kBN - 1 <= qrow || hi <= qrow + 1);
+        s2 = right ? -slope2 : slope2;
+        if (!CAP && !one_side) {
+          // Keys to both sides (around the diagonal, without a causal mask): the scores to the right
+          // take the difference to the left side's bias, in a loop through tensor memory as above.
+          FA_CONVERGED(status);
+          const float per = -2.f * slope2 / softmax_scale;
+#pragma unroll 1
+          for (int c = 0; c < kBN; c += 16) {
+            uint32_t x[16];
+            tmem_ld16(tS + c, x);
+            tmem_ld_wait();
+            reg_fence(x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+              x[e] = __float_as_uint(fmaf(per, static_cast<float>(max(kv0 + c + e - qrow, 0)), __uint_as_float(x[e])));
+            tmem_st16(tS + c, x);
+          }
+          tmem_st_wait();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, sr[q]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 4; ++q) reg_fence(sr[q]);
+          one_side = true;
+        }
+      }
       if constexpr (MOD) {
         if (!__all_sync(0xffffffffu, lo <= kv0 && hi >= kv0 + kBN)) {
           const int first = lo - kv0;
@@ -388,8 +421,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kBN; ++c)
           if (c > lim) sr[c >> 5][c & 31] = 0xff800000u;                  // -inf
       }
-      // ALIBI: every key of the tile lies on one side of the warp's rows
-      const bool one_side = kv0 + kBN - 1 <= qrow - lane || kv0 >= qrow - lane + 31;
       // log2e cap tanh(score / cap) or log2e score, of a pair
       auto scaled = [&](float2 v) {
         if constexpr (CAP) return __fmul2_rn(v, quartic2(v, mods.poly));
@@ -398,13 +429,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_tile;
       if constexpr (ALIBI) {
         // The reference needs no exact maximum, only one that is not far above it: of eight columns
-        // to one side of the warp's rows the largest score and the least bias, at most 7 |slope| log2e
-        // too high.  Slopes for which that is more than the rescaling threshold, and tiles around the
-        // diagonal, take column by column.
+        // the largest score and the least bias, at most 7 |slope| log2e too high.  Slopes for which
+        // that is more than the rescaling threshold take column by column.
         const float d0 = static_cast<float>(qrow - kv0);
         float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
         if (one_side && fabsf(slope2) * 7.f <= kRescaleThreshold) {
-          const float s2 = kv0 >= qrow - lane + 31 ? -slope2 : slope2;   // the bias grows by s2 a column
           const float base = fmaf(-s2, d0, s2 > 0.f ? 7.f * s2 : 0.f);
 #pragma unroll
           for (int c = 0; c < kBN; c += 8) {
@@ -421,8 +450,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float2 v = scaled(make_float2(__uint_as_float(sr[c >> 5][c & 31]),
                                                 __uint_as_float(sr[(c + 1) >> 5][(c + 1) & 31])));
             const float e = d0 - static_cast<float>(c);
-            top[0] = fmaxf(top[0], fmaf(-slope2, fabsf(e), v.x));
-            top[1] = fmaxf(top[1], fmaf(-slope2, fabsf(e - 1.f), v.y));
+            top[0] = fmaxf(top[0], one_side ? fmaf(-s2, e, v.x) : fmaf(-slope2, fabsf(e), v.x));
+            top[1] = fmaxf(top[1], one_side ? fmaf(-s2, e - 1.f, v.y) : fmaf(-slope2, fabsf(e - 1.f), v.y));
           }
         }
         m_tile = fmaxf(top[0], top[1]);
@@ -504,11 +533,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (!ALIBI) {
           exponentials([&](int, float2 sv) { return exponent(sv, neg2); });
         } else {
-          // bias - m: to one side of the rows linear in the column (16 columns by additions from a
-          // product), |i - j| around the diagonal
+          // bias - m: linear in the column, 16 columns by additions from a product (CAP, whose scores
+          // cannot carry a bias: or |i - j| around the diagonal)
           const float d0 = static_cast<float>(qrow - kv0);
-          if (one_side) {
-            const float s2 = kv0 >= qrow - lane + 31 ? -slope2 : slope2;
+          if (!CAP || one_side) {
             float2 bias = make_float2(0.f, 0.f);
             exponentials([&](int c, float2 sv) {
               if (c % 8 == 0) {

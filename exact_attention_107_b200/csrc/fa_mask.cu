@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kThreads) mask_plan_kernel(int* __restrict__ p
   unsigned* starts = reinterpret_cast<unsigned*>(scan_buf + 32);   // [nw] (documents only, as the next two)
   int* last_before = reinterpret_cast<int*>(starts + nw);          // [nw] last run start in the words before
   int* first_after = last_before + nw;                              // [nw] first run start in the words after
+  unsigned* padding = reinterpret_cast<unsigned*>(first_after + nw);   // [nw] rows with a negative id
   const MaskPlan v = mask_plan_view(plan, B, N);
   int2* rows = const_cast<int2*>(v.rows) + static_cast<size_t>(b) * npad;
   int2* order = const_cast<int2*>(v.order) + static_cast<size_t>(b) * nt;
@@ -71,12 +72,22 @@ __global__ void __launch_bounds__(kThreads) mask_plan_kernel(int* __restrict__ p
     tile_hi[t] = 0;
   }
   if (doc != nullptr) {
-#pragma unroll 4
-    for (int w = warp; w < nw; w += kThreads / 32) {
-      const int i = w * 32 + lane;
-      const bool start = i < N && (i == 0 || doc[i] != doc[i - 1]);
-      const unsigned bits = __ballot_sync(0xffffffffu, start);
-      if (lane == 0) starts[w] = bits;
+    for (int w0 = warp; w0 < nw; w0 += 8 * (kThreads / 32)) {
+      int id[8], before[8];                              // eight words' loads in flight
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int i = (w0 + u * (kThreads / 32)) * 32 + lane;
+        id[u] = i < N ? doc[i] : 0;
+        before[u] = lane == 0 && i > 0 && i <= N ? doc[i - 1] : 0;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int w = w0 + u * (kThreads / 32), i = w * 32 + lane;
+        const int left = __shfl_up_sync(0xffffffffu, id[u], 1);
+        const unsigned first = __ballot_sync(0xffffffffu, i < N && (i == 0 || id[u] != (lane == 0 ? before[u] : left)));
+        const unsigned pad = __ballot_sync(0xffffffffu, i < N && id[u] < 0);
+        if (lane == 0 && w < nw) starts[w] = first, padding[w] = pad;
+      }
     }
     __syncthreads();
     // each thread owns `per` consecutive words
@@ -133,7 +144,7 @@ __global__ void __launch_bounds__(kThreads) mask_plan_kernel(int* __restrict__ p
         const unsigned past = lane == 31 ? 0u : bits & (0xffffffffu << (lane + 1));
         lo = upto != 0u ? w * 32 + 31 - __clz(upto) : last_before[w];
         hi = past != 0u ? w * 32 + __ffs(past) - 1 : min(first_after[w], N);
-        if (doc[i] < 0) hi = lo;
+        if ((padding[w] >> lane) & 1u) hi = lo;
       }
       if (causal) hi = min(hi, max(i + 1, pre));
       if (window > 0) {
@@ -157,42 +168,61 @@ __global__ void __launch_bounds__(kThreads) mask_plan_kernel(int* __restrict__ p
   int* k_work = q_work + nt;         // [nt]
   const int nqb = (nt + 1) / 2;
   __syncthreads();
-  for (int t = threadIdx.x; t < nt; t += kThreads) {
-    int4 r = make_int4(0, 0, 0, 0);
-    if (tile_hi[t] > 0) {
-      r.x = tile_lo[t] / 128;
-      r.y = (tile_hi[t] + 127) / 128;
-    }
+  // eight threads an item; whole warps go round, so that the shuffles are full
+  const int part = threadIdx.x & 7;
+  for (int t0 = 0; t0 < nt; t0 += kThreads / 8) {
+    const int t = t0 + static_cast<int>(threadIdx.x >> 3);
     int q_first = INT_MAX, q_end = 0;
-    for (int q = 0; q < nt; ++q) {
-      if (tile_hi[q] > t * 128 && tile_lo[q] < t * 128 + 128) {
-        q_first = min(q_first, q);
-        q_end = q + 1;
+    if (t < nt) {
+      for (int q = part; q < nt; q += 8) {
+        if (tile_hi[q] > t * 128 && tile_lo[q] < t * 128 + 128) {
+          q_first = min(q_first, q);
+          q_end = q + 1;
+        }
       }
     }
-    if (q_end > 0) {
-      r.z = q_first;
-      r.w = q_end;
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) {
+      q_first = min(q_first, __shfl_xor_sync(0xffffffffu, q_first, d));
+      q_end = max(q_end, __shfl_xor_sync(0xffffffffu, q_end, d));
     }
-    tiles[t] = r;
-    k_work[t] = r.w - r.z;
-    q_work[t] = r.y - r.x;
+    if (t < nt && part == 0) {
+      int4 r = make_int4(0, 0, 0, 0);
+      if (tile_hi[t] > 0) {
+        r.x = tile_lo[t] / 128;
+        r.y = (tile_hi[t] + 127) / 128;
+      }
+      if (q_end > 0) {
+        r.z = q_first;
+        r.w = q_end;
+      }
+      tiles[t] = r;
+      k_work[t] = r.w - r.z;
+      q_work[t] = r.y - r.x;
+    }
   }
   __syncthreads();
   int* block_work = k_work + nt;     // [nqb]
   for (int t = threadIdx.x; t < nqb; t += kThreads) block_work[t] = q_work[2 * t] + (2 * t + 1 < nt ? q_work[2 * t + 1] : 0);
   __syncthreads();
   // place of each item: the items with more work, and those with as much before it
-  for (int t = threadIdx.x; t < nt; t += kThreads) {
-    const int kw = k_work[t], qw = t < nqb ? block_work[t] : 0;
+  for (int t0 = 0; t0 < nt; t0 += kThreads / 8) {
+    const int t = t0 + static_cast<int>(threadIdx.x >> 3);
     int k_at = 0, q_at = 0;
-    for (int o = 0; o < nt; ++o) k_at += k_work[o] > kw || (k_work[o] == kw && o < t);
-    order[k_at].x = t;
-    if (t < nqb) {
-      for (int o = 0; o < nqb; ++o) q_at += block_work[o] > qw || (block_work[o] == qw && o < t);
-      order[q_at].y = t;
-    } else {
-      order[t].y = t;                // not a block: never read
+    if (t < nt) {
+      const int kw = k_work[t], qw = t < nqb ? block_work[t] : 0;
+      for (int o = part; o < nt; o += 8) k_at += k_work[o] > kw || (k_work[o] == kw && o < t);
+      if (t < nqb)
+        for (int o = part; o < nqb; o += 8) q_at += block_work[o] > qw || (block_work[o] == qw && o < t);
+    }
+#pragma unroll
+    for (int d = 4; d > 0; d >>= 1) {
+      k_at += __shfl_xor_sync(0xffffffffu, k_at, d);
+      q_at += __shfl_xor_sync(0xffffffffu, q_at, d);
+    }
+    if (t < nt && part == 0) {
+      order[k_at].x = t;
+      order[t < nqb ? q_at : t].y = t;                   // past the blocks: never read
     }
   }
 }
@@ -202,7 +232,7 @@ __global__ void __launch_bounds__(kThreads) mask_plan_kernel(int* __restrict__ p
 cudaError_t launch_mask_plan(int* plan, const int* documents, const int* prefix, int B, int N, int causal, int window,
                              cudaStream_t stream) {
   const size_t nt = (static_cast<size_t>(N) + 127) / 128;
-  const size_t bytes = (2 * nt + 32 + (documents != nullptr ? 3 * 4 * nt : 3 * nt)) * sizeof(int);
+  const size_t bytes = (2 * nt + 32 + (documents != nullptr ? 4 * 4 * nt : 3 * nt)) * sizeof(int);
   cudaError_t e = cudaFuncSetAttribute(mask_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(bytes));
   if (e != cudaSuccess) return e;
