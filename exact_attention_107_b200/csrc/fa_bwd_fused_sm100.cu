@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             } else {
 #pragma unroll
-              for (int c = 0; c < 16; ++c) sr[c] = __float_as_uint(tanh_mufu(__uint_as_float(sr[c]) * cap_in));
+              for (int c = 0; c < 16; ++c) sr[c] = __float_as_uint(tanh_any(__uint_as_float(sr[c]) * cap_in));
             }
           }
 #pragma unroll

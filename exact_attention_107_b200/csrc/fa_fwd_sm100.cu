@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             reg_fence(x);
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float z = __uint_as_float(x[e]) * cap_in, th = tanh_mufu(z), far = quartic_inverse(fabsf(th)) * out_in;
+              const float z = __uint_as_float(x[e]) * cap_in, th = tanh_any(z), far = quartic_inverse(fabsf(th)) * out_in;
               x[e] = mods.poly_limit < 0.f ? __float_as_uint(th)
                      : fabsf(z) <= kTanhPolyLimit ? x[e] : __float_as_uint(copysignf(far, z));
             }

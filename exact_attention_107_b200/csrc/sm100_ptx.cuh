@@ -413,6 +413,12 @@ __device__ __forceinline__ float quartic_inverse(float t) {
 __device__ __forceinline__ float tanh_mufu(float z) {
   return fmaf(2.f, rcp_approx(1.f + ex2_approx(z * -2.88539008177792681472f)), -1.f);
 }
+// tanh for any z: the quartic in its range, which keeps a small z's relative accuracy, else the MUFU.
+__device__ __forceinline__ float tanh_any(float z) {
+  const float u = z * z;
+  const float p = fmaf(fmaf(fmaf(fmaf(kTanhC4, u, kTanhC3), u, kTanhC2), u, kTanhC1), u, kTanhC0);
+  return fabsf(z) <= kTanhPolyLimit ? z * p : tanh_mufu(z);
+}
 // 2^x for a pair: on the FMA pipe when `poly`, else two MUFU ex2.approx.
 __device__ __forceinline__ float2 exp2_pair(float2 x, bool poly) {
   return poly ? exp2_poly2(x) : make_float2(ex2_approx(x.x), ex2_approx(x.y));

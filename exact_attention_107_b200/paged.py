@@ -157,15 +157,14 @@ def paged_attention(q, k_pages, v_pages, block_table, seq_lens, scale: float | N
     status (fa_device_status) to FA_ERR_INDEX.  workspace: for callers that keep one, of
     fa_paged_workspace_size bytes; calls that may overlap on the GPU (other streams, captured
     graphs) must not share it."""
+    if scale is None and isinstance(q, torch.Tensor) and q.dim() == 4:
+        scale = base.default_scale(q.shape[3])
     if stream is None and workspace is None and base._lib is not None:
-        r = base.fast_result(base._fast.decode(
-            q, k_pages, v_pages, block_table, seq_lens, q.shape[-1] ** -0.5 if scale is None else scale, softcap,
-            alibi_slopes, window, None), "fa_paged_attention")
+        r = base.fast_result(base._fast.decode(q, k_pages, v_pages, block_table, seq_lens, scale, softcap,
+                                               alibi_slopes, window, None), "fa_paged_attention")
         if r is not None:
             return r
     args, code = _decode_args(q, k_pages, v_pages, block_table, seq_lens, alibi_slopes)
-    if scale is None:
-        scale = base.default_scale(q.shape[3])
     if workspace is not None:
         _check_workspace(workspace, q.device)
 

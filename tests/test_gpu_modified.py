@@ -83,6 +83,11 @@ CASES = [
     (1, 4, 2, 300, 64, "hot", 3.0, True, "fp16"),
     (1, 2, 2, 400, 64, "steep", 0.0, True, "fp16"),
     (1, 2, 1, 300, 128, "steep-full", 20.0, True, "bf16"),
+    # caps whose polynomial leaves the floats' range, and tiny ones
+    (1, 2, 1, 200, 64, "causal", 2e4, False, "fp16"),
+    (1, 2, 2, 200, 128, "full", 1e9, True, "bf16"),
+    (1, 2, 2, 200, 64, "full", 1e-3, False, "bf16"),
+    (1, 2, 1, 260, 128, "window100-full", 0.2, True, "fp16"),
 ]
 
 
@@ -273,3 +278,53 @@ def test_streams_and_graph():
     for i in (0, 1, 3, 4):
         assert torch.equal(got[i], fresh[i])
     assert ((got[2] - fresh[2]).abs() <= 2 ** -10 * fresh[2].abs() + 1e-6).all()
+
+
+@pytest.mark.parametrize("kind,cap,alibi,dtype", [("doc-padded", 0.0, False, "bf16"), ("causal", 30.0, True, "fp16"),
+                                                  ("prefix", 0.0, True, "bf16"), ("full", 2.0, False, "bf16")])
+def test_both_host_paths_agree(kind, cap, alibi, dtype):
+    """The call marshalled in C++ and the one marshalled in Python (a workspace given, another stream)."""
+    B, H, Hkv, N, D = 2, 4, 2, 190, 64
+    q, k, v, do = (t.cuda() for t in inputs(B, H, Hkv, N, D, dtype, 9))
+    args, causal, _ = mask_args(kind, B, N)
+    more = dict(softcap=cap, alibi_slopes=None if not alibi else slopes_of(H, True).cuda())
+    if args is not None:
+        more["mask"] = fa.attention_mask(B, N, device="cuda", **{n: x.cuda() if isinstance(x, torch.Tensor) else x
+                                                               for n, x in args.items()})
+    here = torch.cuda.current_stream()
+    a, b = fa.attention_forward(q, k, v, 0.2, causal, **more), fa.attention_forward(q, k, v, 0.2, causal, here, **more)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ws = torch.empty(fa.fa_bwd_workspace_size(B, H, N, D), device="cuda", dtype=torch.uint8)
+    ga = fa.attention_backward(q, k, v, *a, do, 0.2, causal, **more)
+    gb = fa.attention_backward(q, k, v, *a, do, 0.2, causal, workspace=ws, **more)
+    assert torch.equal(ga[1], gb[1]) and torch.equal(ga[2], gb[2])
+
+
+def test_refusals_with_gpu_tensors():
+    """What the C++ path hands back is refused by the Python path, with its messages."""
+    q, k, v, do = (t.cuda() for t in inputs(1, 4, 2, 64, 64, "bf16", 1))
+    o, lse = fa.attention_forward(q, k, v, causal=True)
+    mask = fa.attention_mask(1, 64, device="cuda")
+    slopes = torch.ones(4, device="cuda")
+    for error, call in [
+        (TypeError, lambda: fa.attention_forward(q.float(), k.float(), v.float())),
+        (TypeError, lambda: fa.attention_forward(q, k.half(), v)),
+        (ValueError, lambda: fa.attention_forward(q, k, v[:, :1])),
+        (ValueError, lambda: fa.attention_forward(q.transpose(1, 2).contiguous().transpose(1, 2), k, v)),
+        (ValueError, lambda: fa.attention_forward(q, k, v, alibi_slopes=slopes[:2])),
+        (TypeError, lambda: fa.attention_forward(q, k, v, alibi_slopes=slopes.double())),
+        (ValueError, lambda: fa.attention_forward(q, k, v, mask=fa.attention_mask(1, 65, device="cuda"))),
+        (ValueError, lambda: fa.attention_forward(q, k, v, causal=True, mask=mask)),
+        (TypeError, lambda: fa.attention_forward(q, k, v, mask=mask.plan)),
+        (fa.FAError, lambda: fa.attention_forward(q, k, v, softcap=-1.0)),
+        (fa.FAError, lambda: fa.attention_forward(q[:, :3].contiguous(), k, v)),
+        (fa.FAError, lambda: fa.attention_forward(q, k, v, -0.1)),
+        (ValueError, lambda: fa.attention_backward(q, k, v, o, lse[:, :2], do)),
+        (ValueError, lambda: fa.attention_backward(q, k, v, o, lse, do.transpose(1, 2))),
+        (ValueError, lambda: fa.attention_backward(q, k, v, o, lse, do, deterministic=True)),
+    ]:
+        with pytest.raises(error):
+            call()
+    wide = torch.zeros(1, 2, 16, 256, device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(fa.FAError):
+        fa.attention_forward(wide, wide, wide, softcap=1.0)

@@ -306,3 +306,109 @@ def test_layer_prefilled_then_decoded(dtype, D, R, interleaved, cap, alibi):
         ref.check(l, want["lse"][:, :, part], bound["lse"][:, :, part], ("lse", at))
         at += n
     assert at == N
+
+
+def test_pages_before_the_window_are_not_read():
+    """A server that frees the pages that slid out of the window: unset entries there are no error."""
+    B, H, Hkv, T, D, page, window = 2, 8, 2, 3, 128, 16, 70
+    lens = [500, 131]
+    q, kp, vp, bt, sl, _ = decode_inputs(B, H, Hkv, T, D, page, lens, False, "bf16")
+    want = ref.paged_attention(q, kp, vp, bt, sl, 0.1, window=window)
+    for b, n in enumerate(lens):
+        gone = (n - T - window + 1) // page                       # pages wholly before the first row's window
+        for i in range(gone):
+            kp[bt[b, i].item()], vp[bt[b, i].item()] = float("nan"), float("nan")
+            bt[b, i] = -1
+    o, lse = fa.paged_attention(*(t.cuda() for t in (q, kp, vp, bt, sl)), 0.1, window=window)
+    torch.cuda.synchronize()
+    ref.check(o, want[0], want[2])
+    ref.check(lse, want[1], want[3])
+
+
+def test_shared_pages_and_many_empty_sequences():
+    """A common prefix in the same pages for every sequence, most of the batch empty."""
+    B, H, D, page = 300, 2, 64, 16
+    q, kp, vp = rand((B, H, 1, D), "bf16", 1), rand((9, H, page, D), "bf16", 2), rand((9, H, page, D), "bf16", 3)
+    bt = torch.arange(9, dtype=torch.int32).repeat(B, 1)
+    sl = torch.zeros(B, dtype=torch.int32)
+    sl[torch.arange(3, B, 41)] = 139
+    sl[299] = 1
+    want = ref.paged_attention(q, kp, vp, bt, sl, 0.125)
+    o, lse = fa.paged_attention(*(t.cuda() for t in (q, kp, vp, bt, sl)), 0.125)
+    ref.check(o, want[0], want[2])
+    ref.check(lse, want[1], want[3])
+
+
+def test_largest_scores_and_equal_keys():
+    """Scores of hundreds (one key takes all the weight, or all equal keys share it)."""
+    B, H, D, page, n = 1, 4, 64, 16, 1000
+    q, kp, vp, bt, sl, _ = decode_inputs(B, H, H, 1, D, page, [n], False, "fp16")
+    for case in ("hot", "equal"):
+        if case == "hot":
+            q2, k2 = q * 20, kp
+        else:
+            q2, k2 = q, torch.where(torch.isnan(kp), kp, torch.ones_like(kp))
+        for cap in (0.0, 3.0):
+            want = ref.paged_attention(q2, k2, vp, bt, sl, 0.125, cap)
+            o, lse = fa.paged_attention(*(t.cuda() for t in (q2, k2, vp, bt, sl)), 0.125, softcap=cap)
+            ref.check(o, want[0], want[2], case)
+            ref.check(lse, want[1], want[3], case)
+
+
+def test_both_host_paths_agree():
+    """The calls marshalled in C++ and in Python (another stream given, a workspace given)."""
+    B, H, Hkv, T, D, page = 3, 8, 2, 2, 128, 16
+    q, kp, vp, bt, sl, slopes = decode_inputs(B, H, Hkv, T, D, page, [100, 2, 333], True, "bf16")
+    d = [t.cuda() for t in (q, kp, vp, bt, sl)]
+    slopes = slopes.cuda()
+    here = torch.cuda.current_stream()
+    a = fa.paged_attention(*d, softcap=20.0, alibi_slopes=slopes, window=77)
+    b = fa.paged_attention(*d, softcap=20.0, alibi_slopes=slopes, window=77, stream=here)
+    ws = torch.empty(fa.fa_paged_workspace_size(B, H, Hkv, T, D), device="cuda", dtype=torch.uint8)
+    c = fa.paged_attention(*d, softcap=20.0, alibi_slopes=slopes, window=77, workspace=ws)
+    assert all(torch.equal(a[i], b[i]) and torch.equal(a[i], c[i]) for i in (0, 1))
+    table = fa.rotary_table(400, 64).cuda()
+    k = rand((B, T, Hkv, D), "bf16", 5).cuda().transpose(1, 2)
+    pools = [[t.clone() for t in d[1:3]] for _ in range(2)]
+    outs = [fa.paged_append(k, k, *p, d[3], d[4], q=d[0], table=table, stream=s) for p, s in zip(pools, (None, here))]
+    assert torch.equal(*outs) and all(torch.equal(torch.nan_to_num(x), torch.nan_to_num(y)) for x, y in zip(*pools))
+    x, y = fa.rotary_forward(d[0], k, table), fa.rotary_forward(d[0], k, table, stream=here)
+    assert all(torch.equal(i, j) for i, j in zip(x, y))
+
+
+def test_refusals_with_gpu_tensors():
+    """What the C++ path hands back is refused by the Python path, with its messages."""
+    B, H, D, page = 1, 2, 64, 16
+    q, kp, vp, bt, sl, _ = decode_inputs(B, H, H, 1, D, page, [20], False, "bf16")
+    q, kp, vp, bt, sl = (t.cuda() for t in (q, kp, vp, bt, sl))
+    table = fa.rotary_table(40, 64).cuda()
+    odd = torch.zeros(1, 2, 1, 72, device="cuda", dtype=torch.bfloat16)[..., 4:68]
+    for error, call in [
+        (TypeError, lambda: fa.rotary_forward(q.float(), q.float(), table)),
+        (ValueError, lambda: fa.rotary_forward(odd, q, table)),
+        (ValueError, lambda: fa.rotary_forward(q, q[..., :32].contiguous(), table)),
+        (ValueError, lambda: fa.rotary_forward(q, q, table[:, :63].contiguous())),
+        (ValueError, lambda: fa.rotary_forward(q, q, table[:, :32])),
+        (TypeError, lambda: fa.rotary_forward(q, q, table.half())),
+        (TypeError, lambda: fa.rotary_forward(q, q, table, positions=torch.zeros(1, 1, device="cuda", dtype=torch.int64))),
+        (ValueError, lambda: fa.rotary_forward(q, q, table, positions=torch.zeros(2, 1, device="cuda", dtype=torch.int32))),
+        (ValueError, lambda: fa.rotary_forward(q, q, fa.rotary_table(4, 66).cuda())),
+        (TypeError, lambda: fa.paged_append(q, q, kp.half(), vp, bt, sl)),
+        (ValueError, lambda: fa.paged_append(q, q[:, :1], kp, vp, bt, sl)),
+        (ValueError, lambda: fa.paged_append(q, q, kp, vp[:, :1].contiguous(), bt, sl)),
+        (ValueError, lambda: fa.paged_append(q, q, kp, vp, bt[0], sl)),
+        (TypeError, lambda: fa.paged_append(q, q, kp, vp, bt.long(), sl)),
+        (ValueError, lambda: fa.paged_append(q, q, kp, vp, bt, sl, q=q)),
+        (fa.FAError, lambda: fa.paged_append(q, q, kp[:, :, :12].contiguous(), vp[:, :, :12].contiguous(), bt, sl)),
+        (ValueError, lambda: fa.paged_attention(q, kp, vp, bt, sl[None])),
+        (ValueError, lambda: fa.paged_attention(q.expand(2, 2, 1, 64), kp, vp, bt, sl)),
+        (TypeError, lambda: fa.paged_attention(q, kp, vp.float(), bt, sl)),
+        (fa.FAError, lambda: fa.paged_attention(q, kp, vp, bt, sl, -1.0)),
+        (fa.FAError, lambda: fa.paged_attention(q, kp, vp, bt, sl, window=-2)),
+        (fa.FAError, lambda: fa.paged_attention(q[:, :, :0].contiguous(), kp, vp, bt, sl)),
+        (fa.FAError, lambda: fa.paged_attention(q.expand(1, 2, 65, 64).contiguous(), kp, vp, bt, sl)),
+        (fa.FAError, lambda: fa.paged_attention(q, kp, vp, bt, sl, workspace=torch.empty(16, device="cuda", dtype=torch.uint8))),
+        (ValueError, lambda: fa.paged_attention(q, kp, vp, bt, sl, alibi_slopes=torch.ones(3, device="cuda"))),
+    ]:
+        with pytest.raises(error):
+            call()
