@@ -703,14 +703,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the pieces of the unit that begins in CTA blockIdx.x's piece, row blockIdx.y.  Every warp
-// finds the common maximum and the sum over all pieces, a lane for each; the eight warps take every
-// eighth piece's O, a lane D / 32 columns.
-constexpr int kJoinWarps = 8;
+// finds the common maximum and the sum over all pieces, a lane for each; the warps take turns at the
+// pieces' O, a lane D / 32 neighbouring columns.  All latency (an L2 read of what another SM has just
+// written takes most of a microsecond), so O's loads, kFlight pieces a warp, go out before the
+// factors are known.  At D = 256, with twice the registers in flight, half the warps.
+template <int D>
+constexpr int kJoinWarps = D == 256 ? 4 : 8;
 template <int D, int R, bool F16>
-__global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __grid_constant__ PagedLaunch a,
-                                                                     const __grid_constant__ Geometry geo) {
-  constexpr int DP = tile_dim(D), E = D / 32;
-  __shared__ float sh_o[kJoinWarps][D];
+__global__ void __launch_bounds__(32 * kJoinWarps<D>) paged_join_kernel(const __grid_constant__ PagedLaunch a,
+                                                                        const __grid_constant__ Geometry geo) {
+  constexpr int DP = tile_dim(D), E = D / 32, kFlight = D == 256 ? 5 : 10, kWarps = kJoinWarps<D>;
+  __shared__ float sh_o[kWarps][D], sh_f[kMaxCtas];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Workspace ws = workspace_view<DP, R>(a.workspace);
   const Split s = ws.splits[blockIdx.x];
@@ -719,6 +722,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // piece 0 is this CTA's second part, the others are the next CTAs' first
   auto part = [&](int i) { return (static_cast<int>(blockIdx.x) + i) * 2 + (i == 0 ? 1 : 0); };
+  float p[kFlight][E];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int at = i0 + k * kWarps;
+      const float* src = ws.part + (static_cast<size_t>(part(at)) * R + n) * DP + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e) p[k][e] = 0.f;
+      if (at < s.pieces) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) p[k][e] = src[e];
+      }
+    }
+  };
+  load(warp);
   constexpr int kMost = (kMaxCtas + 31) / 32;
   float2 st[kMost];
   float m = -CUDART_INF_F, l = 0.f, o[E] = {};
@@ -728,33 +746,35 @@ __global__ void __launch_bounds__(32 * kJoinWarps) paged_join_kernel(const __gri
     m = fmaxf(m, st[c].x);
   }
   m = redux_max(m);
-  if (m != -CUDART_INF_F) {
+  const float ref = m == -CUDART_INF_F ? 0.f : m;
 #pragma unroll
-    for (int c = 0; c < kMost; ++c) {
-      st[c].x = ex2_approx(st[c].x - m);                       // the piece's factor
-      l = fmaf(st[c].x, st[c].y, l);
-#pragma unroll
-      for (int k = 0; k < 32 / kJoinWarps; ++k) {
-        const int at = warp + k * kJoinWarps, i = c * 32 + at;
-        const float f = __shfl_sync(0xffffffffu, st[c].x, at);
-        if (i >= s.pieces) continue;
-        const float* p = ws.part + (static_cast<size_t>(part(i)) * R + n) * DP;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(f, p[e * 32 + lane], o[e]);
-      }
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  for (int c = 0; c < kMost; ++c) {
+    const float f = ex2_approx(st[c].x - ref);                 // the piece's factor
+    l = fmaf(f, st[c].y, l);
+    if (warp == 0 && c * 32 + lane < s.pieces) sh_f[c * 32 + lane] = f;
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) sh_o[warp][e * 32 + lane] = o[e];
+  for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+  __syncthreads();
+  for (int i0 = warp; i0 < s.pieces; i0 += kWarps * kFlight) {
+    if (i0 != warp) load(i0);
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const int i = i0 + k * kWarps;
+      const float f = i < s.pieces ? sh_f[i] : 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(f, p[k][e], o[e]);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) sh_o[warp][lane * E + e] = o[e];
   __syncthreads();
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const long long row = (static_cast<long long>(s.b) * a.H + s.unit / geo.groups * (a.H / a.Hkv)) * a.T + r0 + n;
-  for (int d = threadIdx.x; d < D; d += 32 * kJoinWarps) {
+  for (int d = threadIdx.x; d < D; d += 32 * kWarps) {
     float sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) sum += sh_o[w][d];
+    for (int w = 0; w < kWarps; ++w) sum += sh_o[w][d];
     a.o[row * D + d] = static_cast<uint16_t>(pack16<F16>(sum * inv, 0.f));
   }
   if (threadIdx.x == 0) a.lse[row] = l == 0.f ? -CUDART_INF_F : (m + log2f(l)) * kLn2;
@@ -796,7 +816,7 @@ cudaError_t launch_impl(const PagedLaunch& a, cudaStream_t stream) {
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, kern, tmQ, tmK, tmV, a, geo)) != cudaSuccess) return e;
   cfg.gridDim = dim3(ctas, geo.M < R ? geo.M : R);
-  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.blockDim = dim3(32 * kJoinWarps<D>);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, R, F16>, a, geo);
 }
