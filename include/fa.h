@@ -323,8 +323,9 @@ size_t fa_paged_workspace_size(int B, int H, int Hkv, int T, int D);
  * lse (B,H,T) float32.  Row t of sequence b has position p = seq_lens[b] - T + t and
  * sees the keys j <= p, with window > 0 only those with p - j < window; x as in
  * fa_fwd_mod with |i - j| = p - j.  A row with p < 0 (a sequence shorter than T, or
- * empty) has O = 0 and lse = -inf.  Table entries past a sequence's last page and the
- * slots behind its last position are never used, whatever they hold.
+ * empty) has O = 0 and lse = -inf.  Table entries past a sequence's last page, or wholly
+ * before every row's window, and the slots behind its last position are never used,
+ * whatever they hold.
  * Lengths beyond the table (table_width * page_size) are cut to it, with FA_ERR_INDEX.
  * workspace: contents ignored and clobbered; calls that may overlap on the GPU need one
  * each.  Results do not vary from run to run. */
