@@ -259,7 +259,9 @@ def modified_backward(q, k, v, o, lse, do, scale, causal, stream, workspace, mas
 
 
 class ModifiedAttention(torch.autograd.Function):
-    """autograd wrapper of the score-modified attention."""
+    """autograd wrapper of the score-modified attention.  Under CUDA graph capture torch's own rule
+    holds: no autograd graph of the same leaves made outside the capture may be alive; the functional
+    calls (attention_forward, attention_backward) have no such rule."""
 
     @staticmethod
     def forward(ctx, q, k, v, scale, causal, mask, softcap, alibi_slopes):

@@ -328,3 +328,45 @@ def test_refusals_with_gpu_tensors():
     wide = torch.zeros(1, 2, 16, 256, device="cuda", dtype=torch.bfloat16)
     with pytest.raises(fa.FAError):
         fa.attention_forward(wide, wide, wide, softcap=1.0)
+
+
+@pytest.mark.parametrize("N,args", [(262144, dict(window=900)), (200001, "documents")])
+def test_longest_sequences(N, args):
+    """The longest plan: sampled rows of the forward and of dQ against 64 bits."""
+    H, D, cap = 2, 64, 20.0
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, k, v, do = (torch.randn(1, h, N, D, device="cuda", generator=g).bfloat16() for h in (H, 1, 1, H))
+    if args == "documents":
+        ids = (torch.arange(N) // 1000).int()
+        ids[150000:150100] = -1
+        lo = (torch.arange(N) // 1000) * 1000
+        lo[150100:151000] = 150100
+        mask = fa.attention_mask(1, N, documents=ids[None].cuda())
+    else:
+        ids, lo = torch.zeros(N), torch.arange(N) - 899
+        mask = fa.attention_mask(1, N, device="cuda", **args)
+    o, lse = fa.attention_forward(q, k, v, mask=mask, softcap=cap)
+    dq, dk, dv = fa.attention_backward(q, k, v, o, lse, do, mask=mask, softcap=cap)
+    u, f = 2.0 ** -8, 2.0 ** -20
+    for i in [0, 1, 127, 128, 899, 999, 1000, 131071, 150050, 150100, 150999, N - 1]:
+        if ids[i] < 0:
+            assert (o[0, :, i] == 0).all() and (dq[0, :, i] == 0).all() and (lse[0, :, i] == float("-inf")).all()
+            continue
+        a = max(0, int(lo[i]))
+        kk, vv = k[0, 0, a:i + 1].double(), v[0, 0, a:i + 1].double()
+        for h in range(H):
+            s = kk @ q[0, h, i].double() / 8.0
+            th = torch.tanh(s / cap)
+            w = torch.softmax(cap * th, 0)
+            e = f * (kk.abs() @ q[0, h, i].double().abs() / 8.0).max() + f * (1 + cap)
+            want, L = w @ vv, torch.logsumexp(cap * th, 0)
+            bound = (2 * e + f + u) * (w @ vv.abs()) + (u + f) * want.abs()
+            assert abs(lse[0, h, i].double() - L) <= e + f * (1 + abs(L))
+            assert ((o[0, h, i].double() - want).abs() <= bound).all()
+            d = do[0, h, i].double()
+            g1 = vv @ d - want @ d
+            ds = w * (1 - th * th) * g1
+            # dS: two roundings and P's error, and what delta takes from O's error
+            dse = (2 * u + 4 * e + 2 * f) * ds.abs() + w * (f * (vv.abs() @ d.abs()) + (d.abs() * bound).sum()) * (1 + 2 * u)
+            grad = ds @ kk / 8.0
+            assert ((dq[0, h, i].double() - grad).abs() <= (dse + f * ds.abs()) @ kk.abs() / 8.0 + u * grad.abs()).all()

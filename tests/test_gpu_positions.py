@@ -412,3 +412,29 @@ def test_refusals_with_gpu_tensors():
     ]:
         with pytest.raises(error):
             call()
+
+
+def test_pool_beyond_32_bit_offsets():
+    """Pages behind the 2^31st element of a pool, appended to and read back."""
+    B, H, Hkv, T, D, page, pages = 2, 16, 8, 40, 128, 256, 8300
+    assert pages * Hkv * page * D > 2 ** 31
+    kp, vp = (torch.empty(pages, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    bt = torch.tensor([[pages - 1, 0, pages - 3], [7, pages - 2, -1]], dtype=torch.int32)
+    q, k, v = (rand((B, 600, h, D), "bf16", s) for s, h in enumerate((H, Hkv, Hkv)))
+    lens = [600, 300]
+    cu = lambda t, a, b: t[:, a:b].contiguous().cuda().transpose(1, 2)
+    for a in range(0, 600, T):                                    # position p of sequence b holds row p
+        new = torch.tensor([max(0, min(T, n - a)) for n in lens], dtype=torch.int32).cuda()
+        at = torch.tensor([min(n, a + T) for n in lens], dtype=torch.int32).cuda()
+        fa.paged_append(cu(k, a, a + T), cu(v, a, a + T), kp, vp, bt.cuda(), at, new_lens=new)
+    sl = torch.tensor(lens, dtype=torch.int32)
+    q1 = q[:, :1].transpose(1, 2).contiguous()
+    o, lse = fa.paged_attention(q1.cuda(), kp, vp, bt.cuda(), sl.cuda())
+    small_k, small_v = (torch.zeros(6, Hkv, page, D, dtype=torch.bfloat16) for _ in range(2))
+    small = torch.tensor([[0, 1, 2], [3, 4, 5]], dtype=torch.int32)
+    for b, n in enumerate(lens):
+        for p in range(n):
+            small_k[small[b, p // page], :, p % page], small_v[small[b, p // page], :, p % page] = k[b, p], v[b, p]
+    want = ref.paged_attention(q1, small_k, small_v, small, sl, ref.default_scale(D))
+    ref.check(o, want[0], want[2])
+    ref.check(lse, want[1], want[3])
