@@ -280,19 +280,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int box_rows = min(kTile, 1 << a.page_shift), pages = kTile / box_rows;
     int fills = 0, u = 0;
     bool ok = true;
-    // This lane's page of a tile: the pool row of its first position, or -1.
-    auto lookup = [&](const Walk& w, int tile) {
+    // This lane's page of a tile: the table's entry is read a tile ahead and looked at only when it is
+    // needed, so that nothing waits for the read; kNone where the lane has none to load.
+    constexpr int kNone = INT_MIN;
+    auto entry = [&](const Walk& w, int tile) {
       const long long j = static_cast<long long>(w.s.tile0 + tile) * kTile + lane * box_rows;
-      if (lane >= pages || j >= w.s.len || j + box_rows <= w.s.first) return -1;
-      const int page = page_of(a.block_table + static_cast<long long>(w.b) * a.table_width, a.table_width, a.page_shift,
-                               a.num_pages, j);
-      if (page < 0) {
-        atomicCAS(a.status, 0, kStatusIndex);
-        return -1;
-      }
-      return static_cast<int>(page_row_of(page, a.Hkv, w.unit / geo.groups, j, a.page_shift));
+      if (lane >= pages || j >= w.s.len || j + box_rows <= w.s.first) return kNone;
+      return max(a.block_table[static_cast<long long>(w.b) * a.table_width + (j >> a.page_shift)], -1);
     };
-    int row = w.more() ? lookup(w, w.tile) : -1;
+    int next = w.more() ? entry(w, w.tile) : kNone;
     while (ok && w.more()) {
       if (kv == 0) {
         const int qbuf = u % L::kBufs;
@@ -309,14 +305,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const int end = w.tile + w.count();
       for (int t = w.tile; ok && t < end; ++t) {
-        const int cur = row;
+        const int page = next;
+        const long long j = static_cast<long long>(w.s.tile0 + t) * kTile + lane * box_rows;
         if (t + 1 < end) {
-          row = lookup(w, t + 1);
+          next = entry(w, t + 1);
         } else {
           Walk n = w;
           n.next(a, geo.units);
-          row = n.more() ? lookup(n, n.tile) : -1;
+          next = n.more() ? entry(n, n.tile) : kNone;
         }
+        // pool row of the page's first position in the tile, or -1
+        int cur = -1;
+        if (page >= 0 && page < a.num_pages) cur = static_cast<int>(page_row_of(page, a.Hkv, w.unit / geo.groups, j, a.page_shift));
+        else if (page != kNone) atomicCAS(a.status, 0, kStatusIndex);
         const unsigned valid = __ballot_sync(0xffffffffu, cur >= 0);
         const uint32_t bytes = static_cast<uint32_t>(__popc(valid)) * box_rows * 128 * L::kPartBoxes;
 #pragma unroll
