@@ -89,7 +89,7 @@ def load_library() -> ctypes.CDLL:
                            "`python -m exact_attention_107_b200.build`") from e
     fast.bind(*(ctypes.cast(getattr(lib, name), vp).value for name in (
         "fa_rotary", "fa_paged_append", "fa_paged_attention", "fa_paged_workspace_size", "fa_fwd_mod", "fa_bwd_mod",
-        "fa_bwd_workspace_size")))
+        "fa_bwd_workspace_size", "fa_mask_plan", "fa_mask_plan_size")))
     _lib, _fast = lib, fast
     return lib
 

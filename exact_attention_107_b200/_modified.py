@@ -128,6 +128,10 @@ def attention_mask(B: int, N: int, *, documents=None, prefix=None, causal: bool 
         raise ValueError("attention_mask needs a CUDA device")
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
+    if stream is None and base._lib is not None:
+        r = base.fast_result(base._fast.mask_plan(documents, prefix, B, N, causal, window, device.index), "attention_mask")
+        if r is not None:
+            return AttentionMask(r[0], B, N)
     size = fa_mask_plan_size(B, N)
     if size == 0:
         raise base.FAError(2, "attention_mask")

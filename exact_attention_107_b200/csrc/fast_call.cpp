@@ -30,6 +30,8 @@ int (*g_fwd)(const void*, const void*, const void*, void*, float*, const void*, 
 int (*g_bwd)(const void*, const void*, const void*, const void*, const void*, const float*, void*, void*, void*, void*,
              size_t, const void*, const float*, float, int, int, int, int, int, float, int, int, void*);
 size_t (*g_bwd_ws)(int, int, int, int);
+int (*g_plan)(void*, size_t, const int*, const int*, int, int, int, int, void*);
+size_t (*g_plan_size)(int, int);
 
 // A call's tensors, checked as they are taken: `ok` turns false at the first that is not ordinary.
 struct Call {
@@ -315,15 +317,32 @@ PyObject* backward(PyObject* const* a, Py_ssize_t n) {
   return st != 0 ? PyLong_FromLong(st) : tuple({dq, dk, dv});
 }
 
+// (documents | None, prefix | None, B, N, causal, window, device index) -> (plan,)
+PyObject* mask_plan(PyObject* const* a, Py_ssize_t n) {
+  if (n != 7 || !g_plan) return back();
+  Call c;
+  const int B = c.whole(a[2]), N = c.whole(a[3]), window = c.whole(a[5]), device = c.whole(a[6]);
+  const bool causal = c.flag(a[4]);
+  c.device = device;
+  const Tensor* documents = c.typed(a[0], at::kInt, 2, true);
+  const Tensor* prefix = c.typed(a[1], at::kInt, 1, true);
+  if (!c.here() || !c.shape(documents, {B, N}) || !c.shape(prefix, {B})) return back();
+  const size_t bytes = g_plan_size(B, N);
+  if (bytes == 0) return back();
+  Tensor plan = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
+  const int st = g_plan(plan.data_ptr(), bytes, ints(documents), ints(prefix), B, N, causal, window, c.stream());
+  return st != 0 ? PyLong_FromLong(st) : tuple({plan});
+}
+
 // bind(addresses of fa_rotary, fa_paged_append, fa_paged_attention, fa_paged_workspace_size, fa_fwd_mod, fa_bwd_mod,
-// fa_bwd_workspace_size)
+// fa_bwd_workspace_size, fa_mask_plan, fa_mask_plan_size)
 PyObject* bind(PyObject* const* a, Py_ssize_t n) {
-  void* at[7];
-  if (n != 7) {
-    PyErr_SetString(PyExc_TypeError, "bind takes seven addresses");
+  void* at[9];
+  if (n != 9) {
+    PyErr_SetString(PyExc_TypeError, "bind takes nine addresses");
     return nullptr;
   }
-  for (int i = 0; i < 7; ++i) {
+  for (int i = 0; i < 9; ++i) {
     at[i] = PyLong_AsVoidPtr(a[i]);
     if (!at[i]) return PyErr_Occurred() ? nullptr : (PyErr_SetString(PyExc_ValueError, "null address"), nullptr);
   }
@@ -334,11 +353,14 @@ PyObject* bind(PyObject* const* a, Py_ssize_t n) {
   g_fwd = reinterpret_cast<decltype(g_fwd)>(at[4]);
   g_bwd = reinterpret_cast<decltype(g_bwd)>(at[5]);
   g_bwd_ws = reinterpret_cast<decltype(g_bwd_ws)>(at[6]);
+  g_plan = reinterpret_cast<decltype(g_plan)>(at[7]);
+  g_plan_size = reinterpret_cast<decltype(g_plan_size)>(at[8]);
   Py_RETURN_NONE;
 }
 
 #define ENTRY(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guard<name>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(rotary), ENTRY(append), ENTRY(decode), ENTRY(forward), ENTRY(backward), ENTRY(bind),
+PyMethodDef methods[] = {ENTRY(rotary), ENTRY(append), ENTRY(decode), ENTRY(forward), ENTRY(backward),
+                         ENTRY(mask_plan), ENTRY(bind),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fast", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

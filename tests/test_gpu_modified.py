@@ -292,6 +292,11 @@ def test_both_host_paths_agree(kind, cap, alibi, dtype):
         more["mask"] = fa.attention_mask(B, N, device="cuda", **{n: x.cuda() if isinstance(x, torch.Tensor) else x
                                                                for n, x in args.items()})
     here = torch.cuda.current_stream()
+    if args is not None:
+        other = fa.attention_mask(B, N, device="cuda", stream=here, **{n: x.cuda() if isinstance(x, torch.Tensor) else x
+                                                                      for n, x in args.items()})
+        used = 8 * (128 + 2) * B * (-(-N // 128))       # past the orders' unused entries nothing is written
+        assert torch.equal(more["mask"].plan[:used], other.plan[:used])
     a, b = fa.attention_forward(q, k, v, 0.2, causal, **more), fa.attention_forward(q, k, v, 0.2, causal, here, **more)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     ws = torch.empty(fa.fa_bwd_workspace_size(B, H, N, D), device="cuda", dtype=torch.uint8)
@@ -325,6 +330,17 @@ def test_refusals_with_gpu_tensors():
     ]:
         with pytest.raises(error):
             call()
+    ids = torch.zeros(2, 16, dtype=torch.int32, device="cuda")
+    for error, kw in [
+        (ValueError, dict(documents=ids[:1])), (TypeError, dict(documents=ids.long())), (ValueError, dict(documents=ids.cpu())),
+        (fa.FAError, dict(prefix=ids[:, 0].contiguous(), causal=False)), (fa.FAError, dict(window=-1, device="cuda")),
+        (fa.FAError, dict(prefix=ids[:, 0].contiguous(), window=3)), (ValueError, dict(prefix=ids[0])),
+    ]:
+        with pytest.raises(error):
+            fa.attention_mask(2, 16, **kw)
+    for B, N in ((0, 4), (1, 0), (1, 262145)):
+        with pytest.raises(fa.FAError):
+            fa.attention_mask(B, N, device="cuda")
     wide = torch.zeros(1, 2, 16, 256, device="cuda", dtype=torch.bfloat16)
     with pytest.raises(fa.FAError):
         fa.attention_forward(wide, wide, wide, softcap=1.0)
