@@ -26,8 +26,8 @@ __host__ __device__ inline WorkItem grouped_order(int cta, int BH, int ntiles, i
   return {g * hg + local % gh, local / gh};
 }
 
-// What the score-modified paths add to a call (fa_mod.cu, and the MOD instances of the forward
-// and fused backward kernels).  All pointers are device pointers.
+// What the score-modified paths add to a call (the MOD instances of the forward and
+// fused backward kernels).  All pointers are device pointers.
 struct ScoreMods {
   const int* plan;      // key intervals and tile ranges (see MaskPlan), or null: full / causal by `causal`
   const float* slopes;  // per query head, or null: no distance bias
@@ -80,7 +80,7 @@ __host__ __device__ inline MaskPlan mask_plan_view(const int* plan, int B, int N
   v.order = reinterpret_cast<const int2*>(v.tiles + B * (npad / 128));
   return v;
 }
-// Builds a plan from optional document ids (B, N) and prefix lengths (B) (fa_mod.cu).
+// Builds a plan from optional document ids (B, N) and prefix lengths (B) (fa_mask.cu).
 cudaError_t launch_mask_plan(int* plan, const int* documents, const int* prefix, int B, int N, int causal, int window,
                              cudaStream_t stream);
 

@@ -13,6 +13,10 @@
 // multiple of 16).  A thread keeps one unit of one token: it unpacks the angles once and turns up
 // to kHeads heads of the token at a time, so that many loads are in flight.  Threads are laid out
 // (unit, head, token): in a token-major input neighbouring threads read neighbouring bytes.
+// Measured: 8 x 4096 tokens of 16 + 4 heads, D = 128, half layout 57 us (5.9 TB/s); 32767 tokens of
+// 8 + 8 heads, interleaved, R = 64: 51 us (5.4 TB/s); append of 5 x 2000 ragged rows 22.8 us.  Half
+// layouts with R not a multiple of 16 are bound by their shared-memory reads of single values: R = 66
+// takes twice R = 128's time.
 #include <cstdint>
 
 #include "fa_internal.h"

@@ -438,3 +438,18 @@ def test_pool_beyond_32_bit_offsets():
     want = ref.paged_attention(q1, small_k, small_v, small, sl, ref.default_scale(D))
     ref.check(o, want[0], want[2])
     ref.check(lse, want[1], want[3])
+
+
+def test_rotary_embedding_of_one_tensor():
+    """Only q or only k, their gradients, and a second backward through them refused."""
+    table = fa.rotary_table(30, 64).cuda()
+    x = rand((2, 2, 30, 64), "bf16", 4).cuda().requires_grad_()
+    flat = torch.arange(30).expand(2, 30)
+    for args in ((x, None), (None, x)):
+        out = [t for t in fa.rotary_embedding(*args, table) if t is not None]
+        assert len(out) == 1
+        g = rand((2, 2, 30, 64), "bf16", 5).cuda()
+        grad, = torch.autograd.grad(out[0], x, g, create_graph=True)
+        ref.check(grad.detach(), *ref.turn(g, table, flat, False, True))
+        with pytest.raises(RuntimeError):
+            grad.float().sum().backward()
