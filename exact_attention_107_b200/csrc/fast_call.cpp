@@ -138,6 +138,13 @@ PyObject* tuple(std::initializer_list<Tensor> ts) {
   return r;
 }
 
+// Allocation and launch run without the interpreter's lock, as torch's own calls do: either may wait
+// for something that another Python thread has to do.
+struct NoLock {
+  PyThreadState* state = PyEval_SaveThread();
+  ~NoLock() { PyEval_RestoreThread(state); }
+};
+
 // Every function: C++ exceptions become Python's.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* guard(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -177,12 +184,15 @@ PyObject* rotary(PyObject* const* a, Py_ssize_t n) {
   const int64_t H = q ? q->size(1) : 0, Hkv = k ? k->size(1) : 0;
   if (B * N > INT_MAX || H + Hkv > 65535 || B * N * D == 0 || (q && H == 0) || (k && Hkv == 0)) return back();
   Tensor qo, ko;
-  if (q) qo = c.empty({B, H, N, D}, c.type);
-  if (k) ko = c.empty({B, Hkv, N, D}, c.type);
-  const int st = g_rotary(ptr(q), ptr(k), q ? qo.data_ptr() : nullptr, k ? ko.data_ptr() : nullptr, floats(table),
+  const int st = [&] {
+    NoLock lock;
+    if (q) qo = c.empty({B, H, N, D}, c.type);
+    if (k) ko = c.empty({B, Hkv, N, D}, c.type);
+    return g_rotary(ptr(q), ptr(k), q ? qo.data_ptr() : nullptr, k ? ko.data_ptr() : nullptr, floats(table),
                           ints(pos), qs, ks, stride, static_cast<int>(table->size(0)), static_cast<int>(B),
                           static_cast<int>(H), static_cast<int>(Hkv), static_cast<int>(N), static_cast<int>(D),
                           static_cast<int>(R), interleaved, inverse, c.code(), c.stream());
+  }();
   return st != 0 ? PyLong_FromLong(st) : tuple({qo, ko});
 }
 
@@ -224,13 +234,16 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
   if (table && (R < 2 || R > D || R % 2 != 0 || rows < 1 || rows > INT_MAX)) return back();
   if (B * T > INT_MAX || H + 2 * Hkv > 65535 || B * T * D * Hkv == 0) return back();
   Tensor qo;
-  if (q) qo = c.empty({B, H, T, D}, c.type);
-  const int st = g_append(
+  const int st = [&] {
+    NoLock lock;
+    if (q) qo = c.empty({B, H, T, D}, c.type);
+    return g_append(
       ptr(k), ptr(v), const_cast<void*>(ptr(cache.k)), const_cast<void*>(ptr(cache.v)), ptr(q), q ? qo.data_ptr() : nullptr,
       ints(cache.table), ints(cache.lens), ints(fresh), floats(table), ks, vs, qs, static_cast<int>(rows),
       static_cast<int>(cache.table->size(1)), static_cast<int>(cache.k->size(0)), static_cast<int>(cache.k->size(2)),
       static_cast<int>(B), static_cast<int>(H), static_cast<int>(Hkv), static_cast<int>(T), static_cast<int>(D),
       static_cast<int>(R), interleaved, c.code(), c.stream());
+  }();
   return st != 0 ? PyLong_FromLong(st) : tuple({qo});
 }
 
@@ -251,13 +264,17 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   const int b = static_cast<int>(B), h = static_cast<int>(H), hk = static_cast<int>(Hkv), t = static_cast<int>(T), d = static_cast<int>(D);
   const size_t bytes = g_decode_ws(b, h, hk, t, d);
   if (bytes == 0) return back();
-  Tensor o = c.empty({B, H, T, D}, c.type), lse = c.empty({B, H, T}, at::kFloat);
-  Tensor ws = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
-  const int st = g_decode(ptr(q), ptr(cache.k), ptr(cache.v), ints(cache.table), ints(cache.lens), o.data_ptr(),
+  Tensor o, lse, ws;
+  const int st = [&] {
+    NoLock lock;
+    o = c.empty({B, H, T, D}, c.type), lse = c.empty({B, H, T}, at::kFloat);
+    ws = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
+    return g_decode(ptr(q), ptr(cache.k), ptr(cache.v), ints(cache.table), ints(cache.lens), o.data_ptr(),
                           static_cast<float*>(lse.data_ptr()), ws.data_ptr(), bytes, floats(slopes),
                           static_cast<float>(cap), window, static_cast<int>(cache.table->size(1)),
                           static_cast<int>(cache.k->size(0)), static_cast<int>(cache.k->size(2)), b, h, hk, t, d,
                           static_cast<float>(scale), c.code(), c.stream());
+  }();
   return st != 0 ? PyLong_FromLong(st) : tuple({o, lse});
 }
 
@@ -287,11 +304,15 @@ PyObject* forward(PyObject* const* a, Py_ssize_t n) {
   const double cap = c.number(a[5]), scale = c.number(a[6]);
   const bool causal = c.flag(a[7]);
   if (!c.here() || (causal && m.plan)) return back();
-  Tensor o = c.empty({m.B, m.H, m.N, m.D}, c.type), lse = c.empty({m.B, m.H, m.N}, at::kFloat);
-  const int st = g_fwd(ptr(m.q), ptr(m.k), ptr(m.v), o.data_ptr(), static_cast<float*>(lse.data_ptr()), ptr(m.plan),
+  Tensor o, lse;
+  const int st = [&] {
+    NoLock lock;
+    o = c.empty({m.B, m.H, m.N, m.D}, c.type), lse = c.empty({m.B, m.H, m.N}, at::kFloat);
+    return g_fwd(ptr(m.q), ptr(m.k), ptr(m.v), o.data_ptr(), static_cast<float*>(lse.data_ptr()), ptr(m.plan),
                        floats(m.slopes), static_cast<float>(cap), static_cast<int>(m.B), static_cast<int>(m.H),
                        static_cast<int>(m.Hkv), static_cast<int>(m.N), static_cast<int>(m.D),
                        static_cast<float>(scale), causal, c.code(), c.stream());
+  }();
   return st != 0 ? PyLong_FromLong(st) : tuple({o, lse});
 }
 
@@ -309,11 +330,15 @@ PyObject* backward(PyObject* const* a, Py_ssize_t n) {
   const int B = static_cast<int>(m.B), H = static_cast<int>(m.H), N = static_cast<int>(m.N), D = static_cast<int>(m.D);
   const size_t bytes = g_bwd_ws(B, H, N, D);
   if (bytes == 0) return back();
-  Tensor dq = c.empty({m.B, m.H, m.N, m.D}, c.type), dk = c.empty({m.B, m.Hkv, m.N, m.D}, c.type);
-  Tensor dv = c.empty({m.B, m.Hkv, m.N, m.D}, c.type), ws = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
-  const int st = g_bwd(ptr(m.q), ptr(m.k), ptr(m.v), ptr(o), ptr(dO), floats(lse), dq.data_ptr(), dk.data_ptr(),
+  Tensor dq, dk, dv, ws;
+  const int st = [&] {
+    NoLock lock;
+    dq = c.empty({m.B, m.H, m.N, m.D}, c.type), dk = c.empty({m.B, m.Hkv, m.N, m.D}, c.type);
+    dv = c.empty({m.B, m.Hkv, m.N, m.D}, c.type), ws = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
+    return g_bwd(ptr(m.q), ptr(m.k), ptr(m.v), ptr(o), ptr(dO), floats(lse), dq.data_ptr(), dk.data_ptr(),
                        dv.data_ptr(), ws.data_ptr(), bytes, ptr(m.plan), floats(m.slopes), static_cast<float>(cap), B, H,
                        static_cast<int>(m.Hkv), N, D, static_cast<float>(scale), causal, c.code(), c.stream());
+  }();
   return st != 0 ? PyLong_FromLong(st) : tuple({dq, dk, dv});
 }
 
@@ -329,8 +354,12 @@ PyObject* mask_plan(PyObject* const* a, Py_ssize_t n) {
   if (!c.here() || !c.shape(documents, {B, N}) || !c.shape(prefix, {B})) return back();
   const size_t bytes = g_plan_size(B, N);
   if (bytes == 0) return back();
-  Tensor plan = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
-  const int st = g_plan(plan.data_ptr(), bytes, ints(documents), ints(prefix), B, N, causal, window, c.stream());
+  Tensor plan;
+  const int st = [&] {
+    NoLock lock;
+    plan = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
+    return g_plan(plan.data_ptr(), bytes, ints(documents), ints(prefix), B, N, causal, window, c.stream());
+  }();
   return st != 0 ? PyLong_FromLong(st) : tuple({plan});
 }
 

@@ -1,4 +1,6 @@
 """Rotary positions and the paged cache on the GPU against their 64-bit forms, element by element."""
+import threading
+
 import pytest
 import torch
 
@@ -453,3 +455,31 @@ def test_rotary_embedding_of_one_tensor():
         ref.check(grad.detach(), *ref.turn(g, table, flat, False, True))
         with pytest.raises(RuntimeError):
             grad.float().sum().backward()
+
+
+def test_calls_from_several_threads():
+    """Eight threads, each on its own stream, at once: every result is the single call's."""
+    B, H, Hkv, T, D, page = 2, 8, 2, 1, 64, 16
+    q, kp, vp, bt, sl, _ = decode_inputs(B, H, Hkv, T, D, page, [700, 90], False, "bf16")
+    d = [t.cuda() for t in (q, kp, vp, bt, sl)]
+    x, table = rand((2, 3, 50, 64), "bf16", 2).cuda(), fa.rotary_table(50, 64).cuda()
+    want = fa.paged_attention(*d) + (fa.rotary_forward(x, None, table)[0],)
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(50):
+                got = fa.paged_attention(*d) + (fa.rotary_forward(x, None, table)[0],)
+            stream.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                bad.append(1)
+            stream.synchronize()
+
+    threads = [threading.Thread(target=work) for _ in range(8)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
