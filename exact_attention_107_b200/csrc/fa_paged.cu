@@ -99,17 +99,8 @@ struct Geometry {
   int M, groups, units;     // query rows of a key-value head; groups of R; units of a sequence
 };
 
-// The positions that a sequence's step reads.
-struct Span {
-  int len, first, tile0, ntiles;
-};
 __device__ __forceinline__ Span span_of(const PagedLaunch& a, int b) {
-  Span s;
-  s.len = min(max(a.seq_lens[b], 0), a.table_width << a.page_shift);
-  s.first = first_seen(s.len - a.T, a.window);
-  s.tile0 = s.first / kTile;
-  s.ntiles = s.len == 0 ? 0 : (s.len + kTile - 1) / kTile - s.tile0;
-  return s;
+  return fa::span_of(a.seq_lens[b], a.table_width << a.page_shift, a.T, a.window, kTile);
 }
 
 // A CTA's piece of the line of tiles, unit by unit; each role walks it by itself.

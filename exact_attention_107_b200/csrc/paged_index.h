@@ -42,4 +42,18 @@ FA_HD AppendSlot append_slot(int len, int fresh, int T, int n, const int* row, i
 // Positions [first, end) that a decode row at position p may see; end = p + 1, or 0 for p < 0.
 FA_HD int first_seen(int p, int window) { return window > 0 && p >= window ? p - window + 1 : 0; }
 
+// The positions that a decode step of T rows reads of a sequence, and the tiles of `tile` that hold
+// them.  Holds for lengths up to the largest int: the tiles are counted from the last position.
+struct Span {
+  int len, first, tile0, ntiles;
+};
+FA_HD Span span_of(int seq_len, int positions, int T, int window, int tile) {
+  Span s;
+  s.len = seq_len < 0 ? 0 : (seq_len < positions ? seq_len : positions);
+  s.first = first_seen(s.len - T, window);
+  s.tile0 = s.first / tile;
+  s.ntiles = s.len == 0 ? 0 : (s.len - 1) / tile + 1 - s.tile0;
+  return s;
+}
+
 }  // namespace fa

@@ -1,0 +1,45 @@
+"""Edges of the rotary, paged-cache and score-modified operators without a GPU: index arithmetic at
+the ends of its range, arguments beyond C's types, and the package without one of its parts."""
+import ctypes
+import shutil
+import subprocess
+from pathlib import Path
+
+import pytest
+
+import exact_attention_107_b200 as fa
+
+CSRC = Path(fa.__file__).resolve().parent / "csrc"
+
+HOST = """
+#include "paged_index.h"
+extern "C" void host_span(int len, int positions, int T, int window, int tile, int* out) {
+  const fa::Span s = fa::span_of(len, positions, T, window, tile);
+  out[0] = s.len, out[1] = s.first, out[2] = s.tile0, out[3] = s.ntiles;
+}
+"""
+
+
+def test_tiles_of_the_longest_caches(tmp_path):
+    """A decode step's span, by the host compiler with signed overflow trapped: lengths up to the
+    largest that a table may have, 2^31 - 8."""
+    cxx = shutil.which("g++")
+    if cxx is None:
+        pytest.skip("no host compiler")
+    (tmp_path / "host.cc").write_text(HOST)
+    subprocess.run([cxx, "-std=c++17", "-O1", "-ftrapv", "-shared", "-fPIC", "-I", str(CSRC), str(tmp_path / "host.cc"),
+                    "-o", str(tmp_path / "host.so")], check=True)
+    lib = ctypes.CDLL(str(tmp_path / "host.so"))
+    out = (ctypes.c_int * 4)()
+    most = 2 ** 31 - 8
+    for length in (-2 ** 31, -1, 0, 1, 127, 128, 129, 5000, most - 128, most - 1, most, 2 ** 31 - 1):
+        for positions in (8, 4096, most):
+            for T in (1, 5, 64):
+                for window in (0, 1, 128, 1000, 2 ** 31 - 1):
+                    lib.host_span(length, positions, T, window, 128, out)
+                    n = min(max(length, 0), positions)
+                    p = n - T                                   # the first row's position
+                    first = p - window + 1 if window and p >= window else 0
+                    tiles = -(-n // 128) - first // 128 if n else 0
+                    assert tuple(out) == (n, first, first // 128, tiles)
+                    assert (first // 128 + tiles) * 128 - 1 <= 2 ** 31 - 1   # the last tile's last position is an int
