@@ -104,6 +104,9 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     p = at.position;
     write = at.page >= 0;
     page_row = page_row_of(at.page, a.Hkv, 0, p, a.page_shift);
+    // A key whose angles the table does not hold stays out of the cache: every thread of the token
+    // decides alike, those of its values and of columns that do not turn too.
+    if (a.R > 0 && p >= a.table_rows) write = false;
     if (here && real && !write) atomicCAS(a.status, 0, kStatusIndex);
   } else if (a.positions != nullptr) {
     p = a.positions[static_cast<long long>(b) * a.position_stride + n];

@@ -80,8 +80,10 @@ def paged_append(k, v, k_pages, v_pages, block_table, seq_lens, *, new_lens=None
     T; None: T); rows t >= n are not written.  With a table (rotary_table) the keys are turned by
     their positions, and so is q (B,H,T,D), whose turned copy is returned (None without q; rows
     t >= n are zero).  k, v and q may be strided.  Two rows that fall on the same slot (sequences
-    that share the page being written) leave either's values there.  A page or position outside its
-    table is not written and sets the device status (fa_device_status) to FA_ERR_INDEX."""
+    that share the page being written) leave a mix of the two there.  A token without a page, or with
+    a table one whose position the table does not hold, is not written, neither its key nor its value;
+    it sets the device status (fa_device_status) to FA_ERR_INDEX.  A row of q whose position the table
+    does not hold comes back unturned."""
     if table is None and q is not None:
         raise ValueError("q is turned on the way and needs a table")
     if stream is None and base._lib is not None:

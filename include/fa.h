@@ -281,7 +281,8 @@ int fa_bwd_mod(const void* q, const void* k, const void* v, const void* o, const
  * a row are contiguous.
  * Index data (positions, pages, lengths) is read on the device: a value outside its
  * table is never followed; the kernel records FA_ERR_INDEX in the device status word
- * and leaves a row at such a position unturned, does not write such a page, and reads
+ * and leaves a row at such a position unturned (in q_out, k_out), does not write a key
+ * and value that have no page or, where keys turn, no row of the rotary table, and reads
  * keys of such a page as absent.
  * ------------------------------------------------------------------------- */
 

@@ -1,0 +1,54 @@
+"""Edges of the rotary, paged-cache and score-modified operators on the GPU: what lies outside a
+table, masked rows of the largest values, single keys, sizes beyond C's integers, both host paths."""
+import pytest
+import torch
+
+import exact_attention_107_b200 as fa
+import exact_attention_107_b200._binding as base
+import operator_refs as ref
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+@pytest.fixture(autouse=True)
+def _need_cuda(cuda_ok):
+    yield
+    assert fa.fa_device_status(reset=True) == 0
+
+
+def rand(shape, dtype, seed, std=1.0):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * std).to(DT[dtype])
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("R,interleaved", [(64, False), (32, False), (34, False), (64, True), (18, True)])
+def test_append_leaves_out_positions_past_the_rotary_table(R, interleaved):
+    """A key whose angles the table does not hold is not written, nor its value; q's row stays unturned."""
+    B, H, Hkv, T, D, page, rows = 3, 3, 2, 3, 64, 16, 20
+    lens = [20, 22, 25]                                  # positions 17-19, 19-21, 22-24
+    table = fa.rotary_table(rows, R)
+    q, k, v = (rand((B, h, T, D), "bf16", s) for s, h in enumerate((H, Hkv, Hkv)))
+    kp, vp = (torch.zeros(2 * B, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    bt = torch.arange(2 * B, dtype=torch.int32).view(B, 2)
+    out = fa.paged_append(k.cuda(), v.cuda(), kp, vp, bt.cuda(), ints(*lens).cuda(), q=q.cuda(), table=table.cuda(),
+                          interleaved=interleaved)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(reset=True) == 13
+    want_k, want_v, bound = (torch.zeros(kp.shape, dtype=torch.float64) for _ in range(3))
+    for b in range(B):
+        for t in range(T):
+            p = lens[b] - T + t
+            one = slice(b, b + 1), slice(None), slice(t, t + 1)
+            if p >= rows:
+                assert torch.equal(out[one].cpu(), q[one])
+                continue
+            ref.check(out[one], *ref.turn(q[one], table, torch.tensor([[p]]), interleaved))
+            at = int(bt[b, p // page]), slice(None), p % page
+            y, e = ref.turn(k[one], table, torch.tensor([[p]]), interleaved)
+            want_k[at], bound[at], want_v[at] = y[0, :, 0], e[0, :, 0], v[b, :, t].double()
+    ref.check(kp, want_k, bound)
+    assert torch.equal(vp.cpu().double(), want_v)
