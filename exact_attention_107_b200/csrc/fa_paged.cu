@@ -488,6 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(bar(L::kBarSEmpty + (i & 1)));
         auto X = [&](int n) { return __uint_as_float(x[n]); };
         if (cap) {
+          // The warp's way to tanh goes by its largest score (the two differ in the last bits), so what
+          // lies in K's rows that no row sees, or is left there from an earlier tile, must not count.
+          if (!live) {
+#pragma unroll
+            for (int n = 0; n < R; ++n) x[n] = 0u;
+          }
           float most = 0.f;
 #pragma unroll
           for (int n = 0; n < R; n += 2) most = fmax3_abs(most, X(n), X(n + 1));

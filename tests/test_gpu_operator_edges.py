@@ -52,3 +52,34 @@ def test_append_leaves_out_positions_past_the_rotary_table(R, interleaved):
             want_k[at], bound[at], want_v[at] = y[0, :, 0], e[0, :, 0], v[b, :, t].double()
     ref.check(kp, want_k, bound)
     assert torch.equal(vp.cpu().double(), want_v)
+
+
+@pytest.mark.parametrize("D,page,T", [(64, 16, 2), (128, 16, 1), (128, 128, 3), (256, 32, 2)])
+def test_capped_decode_does_not_depend_on_unused_slots(D, page, T):
+    """Whatever the slots hold that no row sees, and whatever a call before left on the chip, a capped
+    call's results are the same bit for bit (scores of both sides of the cap's polynomial range)."""
+    B, H, Hkv, lens = 3, 8, 2, [100, 3, 333]
+    wide = -(-max(lens) // page)
+    g = torch.Generator().manual_seed(D)
+    bt = torch.randperm(B * wide, generator=g).int().view(B, wide)
+    q = rand((B, H, T, D), "bf16", 1, 2.0).cuda()
+    pools = [rand((B * wide, Hkv, page, D), "bf16", s) for s in (2, 3)]
+    free = torch.ones(B * wide, page, dtype=torch.bool)
+    for b in range(B):
+        for i in range(lens[b]):
+            free[bt[b, i // page], i % page] = False
+    noise = [rand((B * wide, Hkv, page, D), "bf16", s, 100.0).cuda() for s in (4, 5)]
+    full = ints(*[wide * page] * B).cuda()
+    first = None
+    for fill in (0.0, 1e30, float("nan")):
+        for x in pools:
+            x.transpose(1, 2)[free] = fill
+        kp, vp = (x.cuda() for x in pools)
+        for window in (0, 77):
+            for before in (1.0, 100.0):
+                # leaves keys in shared memory that give large scores
+                fa.paged_attention(q, noise[0] * before, noise[1], bt.cuda(), full)
+                got = fa.paged_attention(q, kp, vp, bt.cuda(), ints(*lens).cuda(), softcap=20.0, window=window)
+                first = first or {}
+                want = first.setdefault(window, got)
+                assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (fill, window, before)
