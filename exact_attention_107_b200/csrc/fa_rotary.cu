@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     // A key whose angles the table does not hold stays out of the cache: every thread of the token
     // decides alike, those of its values and of columns that do not turn too.
     if (a.R > 0 && p >= a.table_rows) write = false;
-    if (here && real && !write) atomicCAS(a.status, 0, kStatusIndex);
+    if (here && ((real && !write) || fresh < 0)) atomicCAS(a.status, 0, kStatusIndex);
   } else if (a.positions != nullptr) {
     p = a.positions[static_cast<long long>(b) * a.position_stride + n];
   }

@@ -77,7 +77,8 @@ def paged_append(k, v, k_pages, v_pages, block_table, seq_lens, *, new_lens=None
     """Writes the keys and values (B,Hkv,T,D) of new tokens into their sequences' pages, in place.
 
     Token t of sequence b takes position seq_lens[b] - n + t with n = new_lens[b] (int32 (B), 0 to
-    T; None: T); rows t >= n are not written.  With a table (rotary_table) the keys are turned by
+    T; None: T; a count outside that writes nothing and sets the status as below); rows t >= n are not
+    written.  With a table (rotary_table) the keys are turned by
     their positions, and so is q (B,H,T,D), whose turned copy is returned (None without q; rows
     t >= n are zero).  k, v and q may be strided.  Two rows that fall on the same slot (sequences
     that share the page being written) leave a mix of the two there.  A token without a page, or with

@@ -304,7 +304,8 @@ int fa_rotary(const void* q, const void* k, void* q_out, void* k_out, const floa
  *   seq_lens    int32 (B): length of each sequence WITH its new tokens.
  *   new_lens    int32 (B), new tokens of each sequence (0 to T), or NULL: T.  Token t
  *               of sequence b has position seq_lens[b] - new_lens[b] + t; rows
- *               t >= new_lens[b] are not written, their q_out rows are zero.
+ *               t >= new_lens[b] are not written, their q_out rows are zero.  A count
+ *               outside 0 to T writes nothing (FA_ERR_INDEX).
  *   table       or NULL with R = 0: nothing turns. */
 int fa_paged_append(const void* k, const void* v, void* k_pages, void* v_pages, const void* q, void* q_out,
                     const int* block_table, const int* seq_lens, const int* new_lens, const float* table,

@@ -83,3 +83,17 @@ def test_capped_decode_does_not_depend_on_unused_slots(D, page, T):
                 first = first or {}
                 want = first.setdefault(window, got)
                 assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]), (fill, window, before)
+
+
+def test_append_reports_negative_counts():
+    """A negative new_lens is outside 0 to T: nothing is written, and the status says so."""
+    B, H, T, D, page = 2, 2, 2, 64, 16
+    k = rand((B, H, T, D), "fp16", 1).cuda()
+    for bad in (-1, -2 ** 31):
+        kp, vp = (torch.zeros(2, H, page, D, dtype=torch.float16, device="cuda") for _ in range(2))
+        out = fa.paged_append(k, k, kp, vp, ints(0, 1)[:, None].cuda(), ints(5, 5).cuda(), new_lens=ints(bad, 1).cuda(),
+                              q=k, table=fa.rotary_table(16, 64).cuda())
+        torch.cuda.synchronize()
+        assert fa.fa_device_status(reset=True) == 13
+        assert (kp[0] == 0).all() and (vp[0] == 0).all() and (out[0] == 0).all()
+        assert torch.equal(vp[1, :, 4], k[1, :, 0]) and (out[1, :, 1] == 0).all()
