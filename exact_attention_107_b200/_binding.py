@@ -302,7 +302,8 @@ def attention_forward(q, k, v, scale: float | None = None, causal: bool = False,
     bf16 and fp16 with head dims up to 128 also take, alone or together, k and v of fewer heads
     (B,Hkv,N,D), an interval mask (attention_mask; instead of causal), softcap > 0 (scores become
     softcap * tanh(score / softcap)) and alibi_slopes (float32 (H); slope * |i - j| is subtracted).
-    A row that sees no key has O = 0 and lse = -inf."""
+    A row that sees no key has O = 0 and lse = -inf.  Masked rows (padding) may hold any finite
+    values, but no NaN or infinity."""
     B, H, N, D = q.shape
     scale = default_scale(D) if scale is None else scale
     if modified(q, k, mask, softcap, alibi_slopes):

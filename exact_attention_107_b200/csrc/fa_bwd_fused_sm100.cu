@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (CAP) {                           // scores -> tanh(s / cap), as in the forward
             float most = 0.f;
 #pragma unroll
-            for (int c = 0; c < 16; c += 2) most = fmax3_abs(most, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
+            for (int c = 0; c < 16; c += 2) most = fmax3_abs_nan(most, __uint_as_float(sr[c]), __uint_as_float(sr[c + 1]));
             if (__all_sync(0xffffffffu, most <= mods.poly_limit)) {
 #pragma unroll
               for (int c = 0; c < 16; c += 2) {
@@ -417,7 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             } else {
 #pragma unroll
-              for (int c = 0; c < 16; ++c) sr[c] = __float_as_uint(tanh_any(__uint_as_float(sr[c]) * cap_in));
+              for (int c = 0; c < 16; ++c)      // NaN becomes finite (see dS): where it counts, lse holds one too
+                sr[c] = __float_as_uint(tanh_any(fminf(fmaxf(__uint_as_float(sr[c]) * cap_in, -20.f), 20.f)));
             }
           }
 #pragma unroll
@@ -493,6 +494,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                          __ffma2_rn(dlp, make_float2(-kWBack, -kWBack),
                                                     kWide ? __fmul2_rn(dpv, make_float2(kWBack, kWBack)) : dpv));
             dsk[c2] = pack16<F16>(ds.x, ds.y);
+            // P = 0 makes dS = 0 also where the products of masked rows have left the fp32 range.
+            if constexpr (MOD) dsk[c2] &= nonzero_f16x2(pp);   // pp is fp16 in either case
           }
         }
         // packed columns [8 hf, 8 hf + 8) of this warpgroup's range (already read: half 0 read

@@ -452,10 +452,21 @@ __device__ __forceinline__ float unpack16_hi(uint32_t x) {
   return __uint_as_float(x & 0xffff0000u);
 }
 
+// 0xffff in each half of a packed fp16 pair that is not zero.
+__device__ __forceinline__ uint32_t nonzero_f16x2(uint32_t x) {
+  return __hne2_mask(*reinterpret_cast<const __half2*>(&x), __half2{});
+}
+
 // Three-input maximum of a and the magnitudes of b and c (one instruction on sm_100).
 __device__ __forceinline__ float fmax3_abs(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
+  return r;
+}
+// The same, NaN where an input is NaN.
+__device__ __forceinline__ float fmax3_abs_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(fabsf(b)), "f"(fabsf(c)));
   return r;
 }
 // Three-input maximum (one instruction on sm_100).

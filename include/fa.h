@@ -239,7 +239,9 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  * over the query heads that share one.  Which keys a row sees is given by a plan
  * (fa_mask_plan, with causal = 0 here), or without one (plan NULL) by `causal`.
  * Values must be finite in every row, masked ones included: a masked key takes
- * weight 0, and 0 times an infinity is not 0 (as in fa_fwd).
+ * weight 0, and 0 times an infinity is not 0 (as in fa_fwd).  Finite ones may be as
+ * large as the type allows: a masked pair's products do not count, even where they
+ * leave the fp32 range.
  * ------------------------------------------------------------------------- */
 
 /* Bytes of a mask plan for B batch elements of N rows; 0 if out of range (N up to

@@ -97,3 +97,33 @@ def test_append_reports_negative_counts():
         assert fa.fa_device_status(reset=True) == 13
         assert (kp[0] == 0).all() and (vp[0] == 0).all() and (out[0] == 0).all()
         assert torch.equal(vp[1, :, 4], k[1, :, 0]) and (out[1, :, 1] == 0).all()
+
+
+@pytest.mark.parametrize("H,Hkv,N,D,cap,alibi,dtype", [
+    (2, 2, 200, 64, 0.0, False, "bf16"), (4, 2, 300, 128, 30.0, False, "bf16"), (3, 1, 200, 96, 0.0, True, "bf16"),
+    (2, 1, 260, 64, 20.0, True, "bf16"), (4, 1, 300, 128, 30.0, True, "fp16")])
+def test_masked_rows_of_the_largest_values(H, Hkv, N, D, cap, alibi, dtype):
+    """Padded rows that hold the type's largest and lowest values (their products with other rows leave
+    the fp32 range): outputs and gradients of the other rows are those of padding with zeros."""
+    q, k, v, do = (rand((2, h, N, D), dtype, s, 1.5) for s, h in enumerate((H, Hkv, Hkv, H)))
+    ids = (torch.arange(N) * 3 // N).int().repeat(2, 1)
+    ids[0, N - 70:] = -1
+    ids[1, 40:90] = -1
+    pad = ids < 0
+    for t in (q, k, v, do):
+        t.transpose(1, 2)[pad] = 0
+    seen = ref.visible(2, N, documents=ids)
+    slopes = torch.tensor([0.4 / (h + 1) for h in range(H)]) if alibi else None
+    want, bound = ref.attention(q, k, v, do, 0.125, seen, cap, slopes)
+    most = torch.finfo(DT[dtype]).max
+    sign = torch.where(torch.arange(D) % 3 == 0, -most, most).to(DT[dtype])
+    for fill in (torch.full((D,), -most, dtype=DT[dtype]), sign):
+        for t in (q, k, v, do):
+            t.transpose(1, 2)[pad] = fill
+        qd, kd, vd, dod = (t.cuda() for t in (q, k, v, do))
+        more = dict(mask=fa.attention_mask(2, N, documents=ids.cuda()), softcap=cap,
+                    alibi_slopes=None if slopes is None else slopes.cuda())
+        o, lse = fa.attention_forward(qd, kd, vd, 0.125, **more)
+        grads = fa.attention_backward(qd, kd, vd, o, lse, dod, 0.125, **more)
+        for name, t in zip(("O", "lse", "dQ", "dK", "dV"), (o, lse, *grads)):
+            ref.check(t, want[name], bound[name], name)
