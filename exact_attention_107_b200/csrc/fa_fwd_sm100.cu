@@ -426,15 +426,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (CAP) return __fmul2_rn(v, quartic2(v, mods.poly));
         return make_float2(v.x * softmax_scale, v.y * softmax_scale);
       };
-      float m_tile;
+      float m_tile, slack = 0.f;                         // the tile's maximum is at most `slack` above m_tile
       if constexpr (ALIBI) {
-        // The reference needs no exact maximum, only one that is not far above it: of eight columns
-        // the largest score and the least bias, at most 7 |slope| log2e too high.  Slopes for which
-        // that is more than the rescaling threshold take column by column.
+        // After its first tile a row's reference needs no exact maximum, only one that is not above it
+        // (that would cost P bits) nor far below: of eight columns the largest score and the greatest
+        // bias against it, at most `slack` too low.  The first reference is exact, so that a row of one
+        // key has P = 1.  Slopes for which the slack is more than the rescaling threshold go column by
+        // column throughout.
         const float d0 = static_cast<float>(qrow - kv0);
         float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
-        if (one_side && fabsf(slope2) * 7.f <= kRescaleThreshold) {
-          const float base = fmaf(-s2, d0, s2 > 0.f ? 7.f * s2 : 0.f);
+        bool exact = !one_side || fabsf(slope2) * 7.f > kRescaleThreshold;
+        if (!exact) {
+          slack = fabsf(slope2) * 7.f;
+          const float base = fmaf(-s2, d0, s2 < 0.f ? 7.f * s2 : 0.f);
 #pragma unroll
           for (int c = 0; c < kBN; c += 8) {
             const int q = c >> 5, e = c & 31;
@@ -444,7 +448,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float bias = fmaf(s2, static_cast<float>(c), base);
             top[(c >> 3) & 1] = fmaxf(top[(c >> 3) & 1], (CAP ? scaled(make_float2(v, v)).x : v * softmax_scale) + bias);
           }
-        } else {
+          exact = __any_sync(0xffffffffu, m == -CUDART_INF_F && fmaxf(top[0], top[1]) > -CUDART_INF_F);
+        }
+        if (exact) {
+          slack = 0.f;
+          top[0] = top[1] = -CUDART_INF_F;
 #pragma unroll
           for (int c = 0; c < kBN; c += 2) {
             const float2 v = scaled(make_float2(__uint_as_float(sr[c >> 5][c & 31]),
@@ -465,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         m_tile = CAP ? scaled(make_float2(most, most)).x : most * scale_log2;
       }
       const float m_new = fmaxf(m, m_tile);
-      const bool need = m_new > m + kRescaleThreshold;                     // always true at j == 0
+      const bool need = m_new + slack > m + kRescaleThreshold;             // always true at j == 0
       const float m_use = need ? m_new : m;
       const float alpha = need ? ex2_approx(m - m_new) : 1.f;
       const float neg = (m_use == -CUDART_INF_F) ? 0.f : -m_use;

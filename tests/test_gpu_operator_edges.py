@@ -127,3 +127,40 @@ def test_masked_rows_of_the_largest_values(H, Hkv, N, D, cap, alibi, dtype):
         grads = fa.attention_backward(qd, kd, vd, o, lse, dod, 0.125, **more)
         for name, t in zip(("O", "lse", "dQ", "dK", "dV"), (o, lse, *grads)):
             ref.check(t, want[name], bound[name], name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D,cap", [(64, 0.0), (128, 0.0), (128, 20.0), (96, 3.0)])
+def test_distance_bias_rows_of_one_key_return_its_value(D, cap, dtype):
+    """A row that sees one key has P = 1: O is that key's value, bit for bit, whatever the slope."""
+    B, H, N = 1, 4, 300
+    q, k, v = (rand((B, H, N, D), dtype, s, 1.5).cuda() for s in range(3))
+    slopes = torch.tensor([0.7, 0.31, 0.05, -0.4]).cuda()
+    each = fa.attention_mask(B, N, documents=torch.arange(N, dtype=torch.int32)[None].cuda())
+    o, _ = fa.attention_forward(q, k, v, mask=each, softcap=cap, alibi_slopes=slopes)
+    assert torch.equal(o, v)
+    o, _ = fa.attention_forward(q, k, v, causal=True, softcap=cap, alibi_slopes=slopes)
+    assert torch.equal(o[:, :, 0], v[:, :, 0])
+
+
+def test_distance_bias_keeps_small_weights():
+    """fp16: keys that weigh 2^-18 of a row's largest count, next to slopes whose bias changes by 7 bits
+    over eight columns (the largest weight is 2^-7 of the largest score with the least bias there)."""
+    N, D, slope = 128, 64, 0.7
+    i = N - 1
+    q = torch.zeros(1, 1, N, D)
+    q[..., 0] = 1.0
+    k = torch.zeros(1, 1, N, D)
+    away = (i - torch.arange(N)).double()
+    k[0, 0, :, 0] = (slope * away - 18 * 0.6931).float()       # every key weighs 2^-18
+    k[0, 0, i - 7, 0] = slope * 7                              # this one 1
+    v = torch.full((1, 1, N, D), 100.0)
+    v[0, 0, i - 7] = 1.0
+    q, k, v = (t.half() for t in (q, k, v))
+    slopes = torch.tensor([slope])
+    want, bound = ref.attention(q, k, v, None, 1.0, ref.visible(1, N), 0.0, slopes)
+    share = want["O"][0, 0, i, 0] - v[0, 0, i - 7, 0].double()
+    assert share > 0.04 and bound["O"][0, 0, i, 0] < share / 8
+    o, lse = fa.attention_forward(q.cuda(), k.cuda(), v.cuda(), 1.0, True, alibi_slopes=slopes.cuda())
+    ref.check(o, want["O"], bound["O"])
+    ref.check(lse, want["lse"], bound["lse"])
