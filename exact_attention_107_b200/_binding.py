@@ -36,6 +36,16 @@ class FAError(RuntimeError):
         super().__init__(f"{where}: {status_string(status)}")
 
 
+class _Int:
+    """An int argument of the C ABI.  ctypes drops the bits beyond C's int (2**32 + 5 would arrive as
+    5); here such a number arrives as the int nearest to it, for the library to accept (a window longer
+    than any sequence) or to refuse (a size, a negative number)."""
+
+    @staticmethod
+    def from_param(n):
+        return ctypes.c_int(max(-2 ** 31, min(int(n), 2 ** 31 - 1)))
+
+
 def load_library() -> ctypes.CDLL:
     """Loads libfa.so (built in-tree by exact_attention_107_b200.build)."""
     global _lib, _fast
@@ -71,7 +81,7 @@ def load_library() -> ctypes.CDLL:
                  "fa_bwd_dq_finish", "fa_mask_plan", "fa_fwd_mod", "fa_bwd_mod", "fa_rotary", "fa_paged_append",
                  "fa_paged_attention"):
         getattr(lib, name).restype = i
-    ll = ctypes.c_longlong
+    ll, i = ctypes.c_longlong, _Int
     lib.fa_mask_plan_size.argtypes = [i, i]
     lib.fa_mask_plan_size.restype = sz
     lib.fa_mask_plan.argtypes = [vp, sz, vp, vp, i, i, i, i, vp]

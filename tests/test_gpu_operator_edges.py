@@ -164,3 +164,25 @@ def test_distance_bias_keeps_small_weights():
     o, lse = fa.attention_forward(q.cuda(), k.cuda(), v.cuda(), 1.0, True, alibi_slopes=slopes.cuda())
     ref.check(o, want["O"], bound["O"])
     ref.check(lse, want["lse"], bound["lse"])
+
+
+def test_windows_beyond_c_integers():
+    """A window longer than any int limits nothing; one below every int is refused like any negative one."""
+    N, D = 300, 64
+    q, k, v = (rand((1, 2, N, D), "bf16", s).cuda() for s in range(3))
+    want = fa.attention_forward(q, k, v, mask=fa.attention_mask(1, N, device="cuda"))
+    here = torch.cuda.current_stream()
+    kp, vp, bt = k[0].view(2, 1, 300, 64)[:, :, :256].contiguous(), v[0].view(2, 1, 300, 64)[:, :, :256].contiguous(), ints(0, 1)[None].cuda()
+    sl, q1 = ints(400).cuda(), q[:, :, :1].contiguous()
+    paged = fa.paged_attention(q1, kp, vp, bt, sl)
+    for window in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63, 10 ** 30):
+        for stream in (None, here):
+            mask = fa.attention_mask(1, N, window=window, device="cuda", stream=stream)
+            assert all(torch.equal(a, b) for a, b in zip(fa.attention_forward(q, k, v, mask=mask), want))
+            got = fa.paged_attention(q1, kp, vp, bt, sl, window=window, stream=stream)
+            assert all(torch.equal(a, b) for a, b in zip(got, paged))
+    for window in (-1, -2 ** 32, -2 ** 32 + 5, -10 ** 30):
+        with pytest.raises(fa.FAError):
+            fa.attention_mask(1, N, window=window, device="cuda")
+        with pytest.raises(fa.FAError):
+            fa.paged_attention(q1, kp, vp, bt, sl, window=window)

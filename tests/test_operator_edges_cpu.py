@@ -43,3 +43,21 @@ def test_tiles_of_the_longest_caches(tmp_path):
                     tiles = -(-n // 128) - first // 128 if n else 0
                     assert tuple(out) == (n, first, first // 128, tiles)
                     assert (first // 128 + tiles) * 128 - 1 <= 2 ** 31 - 1   # the last tile's last position is an int
+
+
+@pytest.mark.parametrize("beyond", [2 ** 31, 2 ** 32 + 1, 2 ** 64 + 1, -2 ** 31 - 1, -2 ** 32 + 1, -10 ** 30])
+def test_integers_beyond_c_are_not_cut(beyond):
+    """ctypes would pass a size of 2^32 + 1 as 1."""
+    P = ctypes.c_void_p(0x10000)                                # never followed: the call is refused before
+    lib = fa.load_library()
+    assert fa.fa_mask_plan_size(1, beyond) == 0
+    assert fa.fa_paged_workspace_size(beyond, 1, 1, 1, 64) == 0 and fa.fa_paged_workspace_size(1, 1, 1, beyond, 64) == 0
+    assert lib.fa_mask_plan(P, 1 << 20, None, None, 1, beyond, 1, 0, None) == 2
+    assert lib.fa_mask_plan(P, 1 << 20, None, None, beyond, 4, 1, 0, None) in (2, 8)
+    s = (ctypes.c_longlong * 3)(64, 64, 64)
+    append = lambda T, rows: lib.fa_paged_append(P, P, P, P, None, None, P, P, None, P, s, s, None, rows, 1, 1, 16, 2, 0, 1, T,
+                                                 64, 64, 0, 0, None)
+    assert append(beyond, 10) == 2
+    if beyond < 0:
+        assert lib.fa_mask_plan(P, 1 << 20, None, None, 1, 4, 1, beyond, None) == 10
+        assert append(1, beyond) == 10
