@@ -46,6 +46,16 @@ class _Int:
         return ctypes.c_int(max(-2 ** 31, min(int(n), 2 ** 31 - 1)))
 
 
+class _Cap:
+    """The cap argument of the C ABI: 0 is none, so a number that only becomes 0 as a float arrives as the
+    smallest float, which the library refuses."""
+
+    @staticmethod
+    def from_param(x):
+        x = float(x)
+        return ctypes.c_float(x if x == 0.0 or abs(x) > 2.0 ** -149 else math.copysign(2.0 ** -149, x))
+
+
 def load_library() -> ctypes.CDLL:
     """Loads libfa.so (built in-tree by exact_attention_107_b200.build)."""
     global _lib, _fast
@@ -85,13 +95,13 @@ def load_library() -> ctypes.CDLL:
     lib.fa_mask_plan_size.argtypes = [i, i]
     lib.fa_mask_plan_size.restype = sz
     lib.fa_mask_plan.argtypes = [vp, sz, vp, vp, i, i, i, i, vp]
-    lib.fa_fwd_mod.argtypes = [vp] * 7 + [f] + [i] * 5 + [f, i, i, vp]
-    lib.fa_bwd_mod.argtypes = [vp] * 10 + [sz, vp, vp, f] + [i] * 5 + [f, i, i, vp]
+    lib.fa_fwd_mod.argtypes = [vp] * 7 + [_Cap] + [i] * 5 + [f, i, i, vp]
+    lib.fa_bwd_mod.argtypes = [vp] * 10 + [sz, vp, vp, _Cap] + [i] * 5 + [f, i, i, vp]
     lib.fa_rotary.argtypes = [vp] * 8 + [ll] + [i] * 10 + [vp]
     lib.fa_paged_append.argtypes = [vp] * 13 + [i] * 12 + [vp]
     lib.fa_paged_workspace_size.argtypes = [i] * 5
     lib.fa_paged_workspace_size.restype = sz
-    lib.fa_paged_attention.argtypes = [vp] * 8 + [sz, vp, f] + [i] * 9 + [f, i, vp]
+    lib.fa_paged_attention.argtypes = [vp] * 8 + [sz, vp, _Cap] + [i] * 9 + [f, i, vp]
     try:
         from . import _fast as fast
     except ImportError as e:

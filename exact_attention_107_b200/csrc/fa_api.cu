@@ -485,6 +485,11 @@ constexpr int kPlanMaxRows = 1 << 18;
 
 bool dtype_ok(int dtype) { return dtype == FA_BF16 || dtype == FA_F16; }
 
+// 0 (none), or a cap for which the kernels' fp32 factors cap log2e and scale / cap exist.
+bool cap_ok(float softcap, float scale) {
+  return softcap == 0.f || (softcap > 0.f && std::isfinite(softcap * 1.4426951f) && std::isfinite(scale / softcap));
+}
+
 // Checks shared by the score-modified forward and backward, and the kernels' view of the mods.
 int mods_args(const int* plan, const float* slopes, float softcap, int B, int H, int Hkv, int N, int D, float scale,
               int causal, int dtype, fa::ScoreMods* m) {
@@ -494,7 +499,7 @@ int mods_args(const int* plan, const float* slopes, float softcap, int B, int H,
   if (plan && N > kPlanMaxRows) return FA_ERR_SHAPE;
   if ((plan && !aligned16(plan)) || (slopes && (reinterpret_cast<uintptr_t>(slopes) & 3u))) return FA_ERR_ALIGN;
   if (!scale_ok(scale) || (causal != 0 && causal != 1) || (plan && causal) || !dtype_ok(dtype)) return FA_ERR_ARG;
-  if (!std::isfinite(softcap) || softcap < 0.f) return FA_ERR_ARG;
+  if (!cap_ok(softcap, scale)) return FA_ERR_ARG;
   m->plan = plan;
   m->slopes = slopes;
   m->softcap = softcap;
@@ -734,7 +739,7 @@ int fa_paged_attention(const void* q, const void* k_pages, const void* v_pages, 
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(o) || !int_aligned(lse) ||
       !int_aligned(block_table) || !int_aligned(seq_lens) || !int_aligned(slopes))
     return FA_ERR_ALIGN;
-  if (!scale_ok(scale) || !std::isfinite(softcap) || softcap < 0.f || window < 0 || !dtype_ok(dtype)) return FA_ERR_ARG;
+  if (!scale_ok(scale) || !cap_ok(softcap, scale) || window < 0 || !dtype_ok(dtype)) return FA_ERR_ARG;
   if (!workspace || workspace_bytes < fa_paged_workspace_size(B, H, Hkv, T, D)) return FA_ERR_WORKSPACE;
   if (!aligned16(workspace)) return FA_ERR_ALIGN;
   fa::PagedLaunch a{};

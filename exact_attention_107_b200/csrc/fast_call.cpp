@@ -90,6 +90,12 @@ struct Call {
     ok = false;
     return 0.0;
   }
+  // A cap: 0, or a number that is none as a float either.
+  float cap(PyObject* o) {
+    const double v = number(o);
+    if (v != 0.0 && static_cast<float>(v) == 0.f) ok = false;
+    return static_cast<float>(v);
+  }
   int whole(PyObject* o) {
     int over = 0;
     const long v = PyLong_CheckExact(o) ? PyLong_AsLongAndOverflow(o, &over) : -1;
@@ -254,7 +260,8 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   const Tensor* q = c.first(a[0]);
   Cache cache;
   if (!q || !q->is_contiguous() || !cache.take(c, a + 1)) return back();
-  const double scale = c.number(a[5]), cap = c.number(a[6]);
+  const double scale = c.number(a[5]);
+  const float cap = c.cap(a[6]);
   const Tensor* slopes = c.typed(a[7], at::kFloat, 1, true);
   const int window = c.whole(a[8]);
   if (a[9] != Py_None || !c.here()) return back();
@@ -271,7 +278,7 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
     ws = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
     return g_decode(ptr(q), ptr(cache.k), ptr(cache.v), ints(cache.table), ints(cache.lens), o.data_ptr(),
                           static_cast<float*>(lse.data_ptr()), ws.data_ptr(), bytes, floats(slopes),
-                          static_cast<float>(cap), window, static_cast<int>(cache.table->size(1)),
+                          cap, window, static_cast<int>(cache.table->size(1)),
                           static_cast<int>(cache.k->size(0)), static_cast<int>(cache.k->size(2)), b, h, hk, t, d,
                           static_cast<float>(scale), c.code(), c.stream());
   }();
@@ -301,7 +308,8 @@ PyObject* forward(PyObject* const* a, Py_ssize_t n) {
   Call c;
   Mods m;
   if (!m.take(c, a, a[3], a[4])) return back();
-  const double cap = c.number(a[5]), scale = c.number(a[6]);
+  const float cap = c.cap(a[5]);
+  const double scale = c.number(a[6]);
   const bool causal = c.flag(a[7]);
   if (!c.here() || (causal && m.plan)) return back();
   Tensor o, lse;
@@ -309,7 +317,7 @@ PyObject* forward(PyObject* const* a, Py_ssize_t n) {
     NoLock lock;
     o = c.empty({m.B, m.H, m.N, m.D}, c.type), lse = c.empty({m.B, m.H, m.N}, at::kFloat);
     return g_fwd(ptr(m.q), ptr(m.k), ptr(m.v), o.data_ptr(), static_cast<float*>(lse.data_ptr()), ptr(m.plan),
-                       floats(m.slopes), static_cast<float>(cap), static_cast<int>(m.B), static_cast<int>(m.H),
+                       floats(m.slopes), cap, static_cast<int>(m.B), static_cast<int>(m.H),
                        static_cast<int>(m.Hkv), static_cast<int>(m.N), static_cast<int>(m.D),
                        static_cast<float>(scale), causal, c.code(), c.stream());
   }();
@@ -322,7 +330,8 @@ PyObject* backward(PyObject* const* a, Py_ssize_t n) {
   Call c;
   Mods m;
   if (!m.take(c, a, a[3], a[4])) return back();
-  const double cap = c.number(a[5]), scale = c.number(a[6]);
+  const float cap = c.cap(a[5]);
+  const double scale = c.number(a[6]);
   const bool causal = c.flag(a[7]);
   const Tensor *o = c.typed(a[8], c.type, 4), *lse = c.typed(a[9], at::kFloat, 3), *dO = c.typed(a[10], c.type, 4);
   if (!c.here() || (causal && m.plan)) return back();
@@ -336,7 +345,7 @@ PyObject* backward(PyObject* const* a, Py_ssize_t n) {
     dq = c.empty({m.B, m.H, m.N, m.D}, c.type), dk = c.empty({m.B, m.Hkv, m.N, m.D}, c.type);
     dv = c.empty({m.B, m.Hkv, m.N, m.D}, c.type), ws = c.empty({static_cast<int64_t>(bytes)}, at::kByte);
     return g_bwd(ptr(m.q), ptr(m.k), ptr(m.v), ptr(o), ptr(dO), floats(lse), dq.data_ptr(), dk.data_ptr(),
-                       dv.data_ptr(), ws.data_ptr(), bytes, ptr(m.plan), floats(m.slopes), static_cast<float>(cap), B, H,
+                       dv.data_ptr(), ws.data_ptr(), bytes, ptr(m.plan), floats(m.slopes), cap, B, H,
                        static_cast<int>(m.Hkv), N, D, static_cast<float>(scale), causal, c.code(), c.stream());
   }();
   return st != 0 ? PyLong_FromLong(st) : tuple({dq, dk, dv});

@@ -230,6 +230,7 @@ int fa_bwd_noalloc(const void* q, const void* k, const void* v, const void* o, c
  * {32, 64, 96, 128}.  For query row i and key j of query head h:
  *     s   = scale * q_i . k_j
  *     x   = softcap * tanh(s / softcap)      (softcap > 0; 0: x = s)
+ *           (softcap log2(e) and scale / softcap have to be finite floats)
  *     x  -= slopes[h] * |i - j|              (slopes given: float32 (H))
  *     P   = softmax of x over the keys that row i sees,  O = P V,
  *     lse = ln(sum over them of exp(x)).

@@ -186,3 +186,38 @@ def test_windows_beyond_c_integers():
             fa.attention_mask(1, N, window=window, device="cuda")
         with pytest.raises(fa.FAError):
             fa.paged_attention(q1, kp, vp, bt, sl, window=window)
+
+
+def test_caps_outside_fp32_are_refused():
+    """A cap that is 0 as a float would leave the scores uncapped, others would divide by nothing."""
+    q = rand((1, 2, 40, 64), "bf16", 1).cuda()
+    kp, bt, sl = q[0].view(2, 1, 40, 64)[:, :, :32].contiguous(), ints(0, 1)[None].cuda(), ints(50).cuda()
+    here = torch.cuda.current_stream()
+    for cap in (1e-50, 1e-45, 1e-40, 3e38, 1e39, -1e-50):
+        for stream in (None, here):
+            with pytest.raises(fa.FAError):
+                fa.attention_forward(q, q, q, softcap=cap, stream=stream)
+            with pytest.raises(fa.FAError):
+                fa.attention_backward(q, q, q, q, q[..., 0].float(), q, softcap=cap, stream=stream)
+            with pytest.raises(fa.FAError):
+                fa.paged_attention(q[:, :, :1].contiguous(), kp, kp, bt, sl, softcap=cap, stream=stream)
+
+
+@pytest.mark.parametrize("cap", [1e-36, 1e-20, 1e30, 2e38])
+def test_caps_at_the_ends_of_fp32(cap):
+    """The smallest caps leave equal weights, the largest the uncapped scores."""
+    B, H, N, D = 1, 2, 150, 64
+    q, k, v, do = (rand((B, H, N, D), "bf16", s) for s in range(4))
+    want, bound = ref.attention(q, k, v, do, 0.125, ref.visible(B, N), cap if cap < 1 else 0.0)
+    d = [t.cuda() for t in (q, k, v, do)]
+    o, lse = fa.attention_forward(*d[:3], 0.125, True, softcap=cap)
+    grads = fa.attention_backward(*d[:3], o, lse, d[3], 0.125, True, softcap=cap)
+    for name, t in zip(("O", "lse", "dQ", "dK", "dV"), (o, lse, *grads)):
+        ref.check(t, want[name], bound[name], name)
+    page = 16
+    kp, vp = (torch.nn.functional.pad(t, (0, 0, 0, 10)).view(B, H, 10, page, D).transpose(1, 2).flatten(0, 1).contiguous().cuda()
+              for t in (k, v))
+    o1, lse1 = fa.paged_attention(d[0][:, :, -1:].contiguous(), kp, vp, torch.arange(10, dtype=torch.int32)[None].cuda(),
+                                  ints(N).cuda(), 0.125, softcap=cap)
+    ref.check(o1, want["O"][:, :, -1:], bound["O"][:, :, -1:])
+    ref.check(lse1, want["lse"][:, :, -1:], bound["lse"][:, :, -1:])

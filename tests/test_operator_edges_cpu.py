@@ -61,3 +61,13 @@ def test_integers_beyond_c_are_not_cut(beyond):
     if beyond < 0:
         assert lib.fa_mask_plan(P, 1 << 20, None, None, 1, 4, 1, beyond, None) == 10
         assert append(1, beyond) == 10
+
+
+@pytest.mark.parametrize("cap", [1e-50, -1e-50, 1e-45, 1e-40, 2.4e38, 3e38, 1e39, float("inf"), float("nan"), -1.0])
+def test_caps_without_finite_factors_are_refused(cap):
+    """softcap log2(e) and scale / softcap as floats; a cap that is 0 only as a float is not "none"."""
+    P = ctypes.c_void_p(0x10000)
+    lib = fa.load_library()
+    assert lib.fa_fwd_mod(P, P, P, P, P, None, None, cap, 1, 2, 1, 256, 64, 0.125, 0, 0, None) == 10
+    assert lib.fa_bwd_mod(P, P, P, P, P, P, P, P, P, P, 1 << 30, None, None, cap, 1, 2, 1, 256, 64, 0.125, 0, 0, None) == 10
+    assert lib.fa_paged_attention(P, P, P, P, P, P, P, P, 1 << 30, None, cap, 0, 4, 10, 16, 1, 2, 1, 1, 64, 0.125, 0, None) == 10
