@@ -11,6 +11,7 @@
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 namespace {
@@ -151,15 +152,13 @@ struct NoLock {
   ~NoLock() { PyEval_RestoreThread(state); }
 };
 
-// Every function: C++ exceptions become Python's.
+// Every function: C++ exceptions become Python's, of the types that torch's own calls raise
+// (torch.OutOfMemoryError for an allocation that fails).
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* guard(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  try {
-    return F(a, n);
-  } catch (const std::exception& e) {
-    PyErr_SetString(PyExc_RuntimeError, e.what());
-    return nullptr;
-  }
+  HANDLE_TH_ERRORS
+  return F(a, n);
+  END_HANDLE_TH_ERRORS
 }
 
 // (q | None, k | None, table, positions | None, interleaved, inverse) -> (q, k)

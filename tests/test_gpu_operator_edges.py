@@ -221,3 +221,14 @@ def test_caps_at_the_ends_of_fp32(cap):
                                   ints(N).cuda(), 0.125, softcap=cap)
     ref.check(o1, want["O"][:, :, -1:], bound["O"][:, :, -1:])
     ref.check(lse1, want["lse"][:, :, -1:], bound["lse"][:, :, -1:])
+
+
+def test_out_of_memory_is_torchs_own_error():
+    """Outputs larger than the card, through both host paths: torch.OutOfMemoryError, and the next call works."""
+    x = rand((1, 1, 1, 256), "bf16", 1).cuda()
+    huge = x.expand(64, 64, 1 << 18, 256)                       # 550 GB as a contiguous result
+    table = fa.rotary_table(8, 256).cuda()
+    for stream in (None, torch.cuda.current_stream()):
+        with pytest.raises(torch.OutOfMemoryError):
+            fa.rotary_forward(huge, None, table, stream=stream)
+    assert torch.equal(fa.rotary_forward(x, None, table)[0], x)  # position 0 turns by nothing
