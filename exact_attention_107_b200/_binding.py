@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import pathlib
+import warnings
 
 import torch
 
@@ -105,13 +106,21 @@ def load_library() -> ctypes.CDLL:
     try:
         from . import _fast as fast
     except ImportError as e:
-        raise RuntimeError("_fast.so is missing or of another torch; build it with "
-                           "`python -m exact_attention_107_b200.build`") from e
-    fast.bind(*(ctypes.cast(getattr(lib, name), vp).value for name in (
-        "fa_rotary", "fa_paged_append", "fa_paged_attention", "fa_paged_workspace_size", "fa_fwd_mod", "fa_bwd_mod",
-        "fa_bwd_workspace_size", "fa_mask_plan", "fa_mask_plan_size")))
+        # Everything works without it: the calls that it takes go through the Python path.
+        warnings.warn(f"_fast.so is missing or of another torch or Python, so small calls take longer ({e}); build it "
+                      "with `python -m exact_attention_107_b200.build`", RuntimeWarning, stacklevel=2)
+        fast = None
+    if fast is not None:
+        fast.bind(*(ctypes.cast(getattr(lib, name), vp).value for name in (
+            "fa_rotary", "fa_paged_append", "fa_paged_attention", "fa_paged_workspace_size", "fa_fwd_mod", "fa_bwd_mod",
+            "fa_bwd_workspace_size", "fa_mask_plan", "fa_mask_plan_size")))
     _lib, _fast = lib, fast
     return lib
+
+
+def fast_path(stream) -> bool:
+    """Whether a call may go to _fast, which launches on the current stream."""
+    return stream is None and _lib is not None and _fast is not None
 
 
 def fast_result(r, where: str):

@@ -128,7 +128,7 @@ def attention_mask(B: int, N: int, *, documents=None, prefix=None, causal: bool 
         raise ValueError("attention_mask needs a CUDA device")
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
-    if stream is None and base._lib is not None:
+    if base.fast_path(stream):
         r = base.fast_result(base._fast.mask_plan(documents, prefix, B, N, causal, window, device.index), "attention_mask")
         if r is not None:
             return AttentionMask(r[0], B, N)
@@ -223,7 +223,7 @@ def _fits(mask, q):
 
 
 def modified_forward(q, k, v, scale, causal, stream, mask, softcap, alibi_slopes):
-    if stream is None and base._lib is not None and _fits(mask, q):
+    if base.fast_path(stream) and _fits(mask, q):
         r = base.fast_result(base._fast.forward(q, k, v, None if mask is None else mask.plan, alibi_slopes, softcap,
                                                 scale, causal), "fa_fwd_mod")
         if r is not None:
@@ -239,7 +239,7 @@ def modified_forward(q, k, v, scale, causal, stream, mask, softcap, alibi_slopes
 
 
 def modified_backward(q, k, v, o, lse, do, scale, causal, stream, workspace, mask, softcap, alibi_slopes):
-    if stream is None and workspace is None and base._lib is not None and _fits(mask, q):
+    if base.fast_path(stream) and workspace is None and _fits(mask, q):
         r = base.fast_result(base._fast.backward(q, k, v, None if mask is None else mask.plan, alibi_slopes, softcap,
                                                  scale, causal, o, lse, do), "fa_bwd_mod")
         if r is not None:

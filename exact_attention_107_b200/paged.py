@@ -87,7 +87,7 @@ def paged_append(k, v, k_pages, v_pages, block_table, seq_lens, *, new_lens=None
     does not hold comes back unturned."""
     if table is None and q is not None:
         raise ValueError("q is turned on the way and needs a table")
-    if stream is None and base._lib is not None:
+    if base.fast_path(stream):
         r = base.fast_result(base._fast.append(k, v, k_pages, v_pages, block_table, seq_lens, new_lens, q, table,
                                                interleaved), "fa_paged_append")
         if r is not None:
@@ -162,7 +162,7 @@ def paged_attention(q, k_pages, v_pages, block_table, seq_lens, scale: float | N
     graphs) must not share it."""
     if scale is None and isinstance(q, torch.Tensor) and q.dim() == 4:
         scale = base.default_scale(q.shape[3])
-    if stream is None and workspace is None and base._lib is not None:
+    if base.fast_path(stream) and workspace is None:
         r = base.fast_result(base._fast.decode(q, k_pages, v_pages, block_table, seq_lens, scale, softcap,
                                                alibi_slopes, window, None), "fa_paged_attention")
         if r is not None:

@@ -142,7 +142,7 @@ def fa_rotary(q, k, q_out, k_out, table, positions=None, interleaved: bool = Fal
 
 
 def _turn(q, k, table, positions, interleaved, inverse, stream):
-    if stream is None and base._lib is not None:
+    if base.fast_path(stream):
         r = base.fast_result(base._fast.rotary(q, k, table, positions, interleaved, inverse), "fa_rotary")
         if r is not None:
             return r

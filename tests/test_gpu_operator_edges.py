@@ -232,3 +232,26 @@ def test_out_of_memory_is_torchs_own_error():
         with pytest.raises(torch.OutOfMemoryError):
             fa.rotary_forward(huge, None, table, stream=stream)
     assert torch.equal(fa.rotary_forward(x, None, table)[0], x)  # position 0 turns by nothing
+
+
+def test_results_without_the_module_of_the_small_calls(monkeypatch):
+    """Every operator through the Python path alone: the same results."""
+    B, H, Hkv, N, D = 2, 4, 2, 60, 64
+    q, k, v, do = (rand((B, h, N, D), "fp16", s).cuda() for s, h in enumerate((H, Hkv, Hkv, H)))
+    table, ids = fa.rotary_table(N, D).cuda(), (torch.arange(N) // 25).int().repeat(B, 1).cuda()
+    bt = torch.arange(8, dtype=torch.int32).view(B, 4).cuda()
+
+    def step():
+        mask = fa.attention_mask(B, N, documents=ids)
+        out = fa.attention_forward(q, k, v, mask=mask, softcap=10.0)
+        dq, dk, dv = fa.attention_backward(q, k, v, *out, do, mask=mask, softcap=10.0)
+        kp, vp = (torch.zeros(8, Hkv, 16, D, dtype=torch.float16, device="cuda") for _ in range(2))
+        qn = fa.paged_append(k, v, kp, vp, bt, ints(N, N).cuda(), q=q, table=table)
+        last = fa.paged_attention(qn[:, :, -1:].contiguous(), kp, vp, bt, ints(N, N).cuda())
+        return (*out, dk, dv, qn, kp, vp, *last, *fa.rotary_forward(q, k, table))
+
+    fa.load_library()
+    assert base._fast is not None
+    want = step()
+    monkeypatch.setattr(base, "_fast", None)
+    assert all(torch.equal(a, b) for a, b in zip(step(), want))

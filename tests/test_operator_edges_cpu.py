@@ -3,12 +3,14 @@ the ends of its range, arguments beyond C's types, and the package without one o
 import ctypes
 import shutil
 import subprocess
+import sys
 from pathlib import Path
 
 import pytest
 
 import exact_attention_107_b200 as fa
 
+ROOT = Path(__file__).resolve().parents[1]
 CSRC = Path(fa.__file__).resolve().parent / "csrc"
 
 HOST = """
@@ -71,3 +73,30 @@ def test_caps_without_finite_factors_are_refused(cap):
     assert lib.fa_fwd_mod(P, P, P, P, P, None, None, cap, 1, 2, 1, 256, 64, 0.125, 0, 0, None) == 10
     assert lib.fa_bwd_mod(P, P, P, P, P, P, P, P, P, P, 1 << 30, None, None, cap, 1, 2, 1, 256, 64, 0.125, 0, 0, None) == 10
     assert lib.fa_paged_attention(P, P, P, P, P, P, P, P, 1 << 30, None, cap, 0, 4, 10, 16, 1, 2, 1, 1, 64, 0.125, 0, None) == 10
+
+
+def python(code):
+    r = subprocess.run([sys.executable, "-W", "always", "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    return r
+
+
+def test_the_library_serves_without_the_module_of_the_small_calls():
+    """_fast.so belongs to one build of torch; without it everything goes through the Python path."""
+    r = python("""
+import sys
+sys.modules["exact_attention_107_b200._fast"] = None       # importing it raises ImportError
+import torch
+import exact_attention_107_b200 as fa
+import exact_attention_107_b200._binding as base
+assert fa.fa_version() > 0 and base._fast is None and not base.fast_path(None)
+q = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+for call in (lambda: fa.rotary_forward(q, q, fa.rotary_table(4, 64)), lambda: fa.attention_forward(q, q, q, softcap=1.0)):
+    try:
+        call()
+    except ValueError as e:
+        assert "CUDA" in str(e)
+    else:
+        raise SystemExit("not refused")
+""")
+    assert "_fast.so is missing" in r.stderr
