@@ -27,8 +27,10 @@ TIMEOUT_TEST_LIB = PKG / "libfa_timeout_test.so"
 # Debug build: device-side bounds checks of computed indices and warp-convergence checks at
 # the warp-collective tensor-memory phases (a failed check records FA_ERR_DEBUG_CHECK).
 DEBUG_LIB = PKG / "libfa_debug.so"
-# CPython extension with the host side of the small calls (csrc/fast_call.cpp).
+# CPython extension with the host side of the small calls (csrc/fast_call.cpp), and the torch and
+# Python that it was built for.
 FAST_MODULE = PKG / "_fast.so"
+FAST_STAMP = BUILD / "fast.stamp"
 VARIANTS = {"timeout_test": ["-DFA_WAIT_LIMIT_CYCLES=100"], "debug": ["-DFA_DEBUG_CHECKS"]}
 SOURCES = ["fa_api.cu", "fa_fwd_sm100.cu", "fa_fwd_d256_sm100.cu", "fa_fwd_f32.cu", "fa_bwd_sm100.cu",
            "fa_bwd_d256_sm100.cu", "fa_bwd_fused_sm100.cu", "fa_noalloc.cu", "fa_mask.cu", "fa_rotary.cu",
@@ -54,6 +56,17 @@ def up_to_date() -> bool:
         return False
     t = min(lib.stat().st_mtime for lib in libs)
     return all(p.stat().st_mtime <= t for p in _deps())
+
+
+def fast_stamp() -> str:
+    """What _fast.so depends on besides its sources."""
+    import importlib.metadata
+    import sysconfig
+    return f"torch {importlib.metadata.version('torch')} {sysconfig.get_config_var('SOABI')}"
+
+
+def fast_fits() -> bool:
+    return FAST_STAMP.exists() and FAST_STAMP.read_text() == fast_stamp()
 
 
 def _compile(src: str, verbose: bool, ptxas_v: bool, variant: str = "") -> pathlib.Path:
@@ -91,6 +104,8 @@ def _compile_fast(verbose: bool) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for fast_call.cpp:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, FAST_MODULE)
+    FAST_STAMP.parent.mkdir(exist_ok=True)
+    FAST_STAMP.write_text(fast_stamp())
 
 
 def _link(objs, lib: pathlib.Path, verbose: bool) -> None:
@@ -109,6 +124,8 @@ def build(force: bool = False, verbose: bool = False, ptxas_v: bool = False) -> 
     test-only libfa_timeout_test.so (the same sources with short pipeline-wait limits) and
     libfa_debug.so (the same sources with device-side bounds and convergence checks)."""
     if not force and not ptxas_v and up_to_date():
+        if not fast_fits():
+            _compile_fast(verbose)
         return LIB
     BUILD.mkdir(exist_ok=True)
     jobs = [(s, v) for v in ("", "timeout_test", "debug") for s in SOURCES]

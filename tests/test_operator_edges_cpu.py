@@ -9,6 +9,7 @@ from pathlib import Path
 import pytest
 
 import exact_attention_107_b200 as fa
+from exact_attention_107_b200 import build
 
 ROOT = Path(__file__).resolve().parents[1]
 CSRC = Path(fa.__file__).resolve().parent / "csrc"
@@ -88,6 +89,7 @@ import sys
 sys.modules["exact_attention_107_b200._fast"] = None       # importing it raises ImportError
 import torch
 import exact_attention_107_b200 as fa
+from exact_attention_107_b200 import build
 import exact_attention_107_b200._binding as base
 assert fa.fa_version() > 0 and base._fast is None and not base.fast_path(None)
 q = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
@@ -100,3 +102,27 @@ for call in (lambda: fa.rotary_forward(q, q, fa.rotary_table(4, 64)), lambda: fa
         raise SystemExit("not refused")
 """)
     assert "_fast.so is missing" in r.stderr
+
+
+def test_another_torch_rebuilds_the_module_of_the_small_calls(tmp_path, monkeypatch):
+    """Nothing but _fast.so depends on torch: a new one makes build() compile that, and only that."""
+    calls = []
+    monkeypatch.setattr(build, "up_to_date", lambda: True)
+    monkeypatch.setattr(build, "FAST_STAMP", tmp_path / "_build" / "fast.stamp")
+    monkeypatch.setattr(build, "FAST_MODULE", tmp_path / "_fast.so")
+    monkeypatch.setattr(build, "_compile", lambda *a: calls.append("cuda"))
+
+    def run(cmd, **kw):
+        calls.append("fast")
+        Path(cmd[cmd.index("-o") + 1]).write_text("")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    build.build()
+    assert calls == ["fast"] and (tmp_path / "_fast.so").exists()
+    build.build()
+    assert calls == ["fast"]
+    monkeypatch.setattr(build, "fast_stamp", lambda: "torch 99 cpython-399")
+    build.build()
+    build.build()
+    assert calls == ["fast", "fast"]
