@@ -96,7 +96,7 @@ def _compile_fast(verbose: bool) -> None:
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I" + str(root / "include"), "-I" + str(root / "include/torch/csrc/api/include"),
-           "-I" + str(cuda / "include"), "-I" + sysconfig.get_paths()["include"], str(CSRC / "fast_call.cpp"),
+           "-I" + str(cuda / "include"), "-I" + sysconfig.get_paths()["include"], "-I" + str(INCLUDE), str(CSRC / "fast_call.cpp"),
            "-o", str(tmp), "-L" + str(root / "lib"), "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
     if verbose:
         print(" ".join(cmd), flush=True)

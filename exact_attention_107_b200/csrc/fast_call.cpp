@@ -14,25 +14,22 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include "fa.h"
+
 namespace {
 
 using at::Tensor;
 
-int (*g_rotary)(const void*, const void*, void*, void*, const float*, const int*, const long long*, const long long*,
-                long long, int, int, int, int, int, int, int, int, int, int, void*);
-int (*g_append)(const void*, const void*, void*, void*, const void*, void*, const int*, const int*, const int*,
-                const float*, const long long*, const long long*, const long long*, int, int, int, int, int, int, int,
-                int, int, int, int, int, void*);
-int (*g_decode)(const void*, const void*, const void*, const int*, const int*, void*, float*, void*, size_t,
-                const float*, float, int, int, int, int, int, int, int, int, int, float, int, void*);
-size_t (*g_decode_ws)(int, int, int, int, int);
-int (*g_fwd)(const void*, const void*, const void*, void*, float*, const void*, const float*, float, int, int, int, int,
-             int, float, int, int, void*);
-int (*g_bwd)(const void*, const void*, const void*, const void*, const void*, const float*, void*, void*, void*, void*,
-             size_t, const void*, const float*, float, int, int, int, int, int, float, int, int, void*);
-size_t (*g_bwd_ws)(int, int, int, int);
-int (*g_plan)(void*, size_t, const int*, const int*, int, int, int, int, void*);
-size_t (*g_plan_size)(int, int);
+// The declarations give the types, so that a changed signature does not compile here.
+decltype(&fa_rotary) g_rotary;
+decltype(&fa_paged_append) g_append;
+decltype(&fa_paged_attention) g_decode;
+decltype(&fa_paged_workspace_size) g_decode_ws;
+decltype(&fa_fwd_mod) g_fwd;
+decltype(&fa_bwd_mod) g_bwd;
+decltype(&fa_bwd_workspace_size) g_bwd_ws;
+decltype(&fa_mask_plan) g_plan;
+decltype(&fa_mask_plan_size) g_plan_size;
 
 // A call's tensors, checked as they are taken: `ok` turns false at the first that is not ordinary.
 struct Call {
@@ -252,9 +249,9 @@ PyObject* append(PyObject* const* a, Py_ssize_t n) {
   return st != 0 ? PyLong_FromLong(st) : tuple({qo});
 }
 
-// (q, k_pages, v_pages, block_table, seq_lens, scale, softcap, slopes | None, window, workspace | None) -> (o, lse)
+// (q, k_pages, v_pages, block_table, seq_lens, scale, softcap, slopes | None, window) -> (o, lse)
 PyObject* decode(PyObject* const* a, Py_ssize_t n) {
-  if (n != 10 || !g_decode) return back();
+  if (n != 9 || !g_decode) return back();
   Call c;
   const Tensor* q = c.first(a[0]);
   Cache cache;
@@ -263,7 +260,7 @@ PyObject* decode(PyObject* const* a, Py_ssize_t n) {
   const float cap = c.cap(a[6]);
   const Tensor* slopes = c.typed(a[7], at::kFloat, 1, true);
   const int window = c.whole(a[8]);
-  if (a[9] != Py_None || !c.here()) return back();
+  if (!c.here()) return back();
   const int64_t B = q->size(0), H = q->size(1), T = q->size(2), D = q->size(3), Hkv = cache.k->size(1);
   if (cache.k->size(3) != D || !c.shape(cache.lens, {B}) || cache.table->size(0) != B || !c.shape(slopes, {H})) return back();
   if (B > INT_MAX || H > INT_MAX || T > INT_MAX || Hkv > INT_MAX) return back();

@@ -164,7 +164,7 @@ def paged_attention(q, k_pages, v_pages, block_table, seq_lens, scale: float | N
         scale = base.default_scale(q.shape[3])
     if base.fast_path(stream) and workspace is None:
         r = base.fast_result(base._fast.decode(q, k_pages, v_pages, block_table, seq_lens, scale, softcap,
-                                               alibi_slopes, window, None), "fa_paged_attention")
+                                               alibi_slopes, window), "fa_paged_attention")
         if r is not None:
             return r
     args, code = _decode_args(q, k_pages, v_pages, block_table, seq_lens, alibi_slopes)
