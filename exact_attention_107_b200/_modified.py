@@ -10,8 +10,9 @@ from torch.autograd.function import once_differentiable
 from . import _binding as base
 
 DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1}
-_device_now = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# Not there in a torch without CUDA, where no call gets as far as to need them.
+_device_now = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def stream_here(device, stream):

@@ -126,3 +126,21 @@ def test_another_torch_rebuilds_the_module_of_the_small_calls(tmp_path, monkeypa
     build.build()
     build.build()
     assert calls == ["fast", "fast"]
+
+
+def test_import_under_a_torch_without_cuda():
+    """Which lacks the CUDA bindings: importing works, a call is refused for its tensors."""
+    python("""
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    delattr(torch._C, name)
+import exact_attention_107_b200 as fa
+assert fa.rotary_table(4, 8).shape == (4, 8)
+q = torch.zeros(1, 2, 4, 64, dtype=torch.bfloat16)
+try:
+    fa.attention_forward(q, q, q, softcap=1.0)
+except ValueError as e:
+    assert "CUDA" in str(e)
+else:
+    raise SystemExit("not refused")
+""")
