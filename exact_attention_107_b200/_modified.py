@@ -85,10 +85,19 @@ def ptr(t):
 # ----------------------------------------------------------------------------- masks
 class AttentionMask:
     """Which keys each row may see, for B batch elements of N rows: the plan of fa_mask_plan on
-    its device.  Made by attention_mask; any number of calls may use it."""
+    its device.  Made by attention_mask; any number of calls may use it, on any stream that runs
+    after the one it was made on, and it may be dropped as soon as the last of them has returned."""
 
-    def __init__(self, plan: torch.Tensor, B: int, N: int):
+    def __init__(self, plan: torch.Tensor, B: int, N: int, raw=None):
         self.plan, self.B, self.N = plan, B, N
+        self._known = {raw}                      # raw streams that the plan's memory is kept for
+
+    def used_on(self, raw) -> None:
+        """Keeps the plan's memory from being handed out again before what runs on the stream now has
+        read it: callers hold a mask, not its memory, so they cannot do it."""
+        if raw not in self._known:
+            self.plan.record_stream(torch.cuda.ExternalStream(raw, device=self.plan.device))
+            self._known.add(raw)
 
 
 def fa_mask_plan_size(B: int, N: int) -> int:
@@ -112,7 +121,7 @@ def _mask_plan(raw, keep, pp, pn, documents, prefix, B, N, causal, window):
 
 
 def _new_plan(raw, keep, device, size):
-    return keep(torch.empty(size, device=device, dtype=torch.uint8))
+    return keep(torch.empty(size, device=device, dtype=torch.uint8)), raw
 
 
 def attention_mask(B: int, N: int, *, documents=None, prefix=None, causal: bool = True, window: int = 0, device=None,
@@ -132,13 +141,13 @@ def attention_mask(B: int, N: int, *, documents=None, prefix=None, causal: bool 
     if base.fast_path(stream):
         r = base.fast_result(base._fast.mask_plan(documents, prefix, B, N, causal, window, device.index), "attention_mask")
         if r is not None:
-            return AttentionMask(r[0], B, N)
+            return AttentionMask(r[0], B, N, _raw_stream(device.index))
     size = fa_mask_plan_size(B, N)
     if size == 0:
         raise base.FAError(2, "attention_mask")
-    plan = on(device, stream, _new_plan, device, size)
+    plan, raw = on(device, stream, _new_plan, device, size)
     fa_mask_plan(plan, documents, prefix, B, N, causal, window, stream)
-    return AttentionMask(plan, B, N)
+    return AttentionMask(plan, B, N, raw)
 
 
 # ----------------------------------------------------------------------------- C-ABI calls
@@ -176,10 +185,12 @@ def fa_fwd_mod(q, k, v, o, lse, scale: float, causal: bool, mask=None, softcap: 
     B, H, _, N, D, code, mods = _mod_args(q, k, v, mask, softcap, alibi_slopes, causal)
     check_on(o, "o", q.dtype, (B, H, N, D), q.device)
     check_on(lse, "lse", torch.float32, (B, H, N), q.device)
-    on(q.device, stream, _fwd, q, k, v, o, lse, mods, scale, causal, code)
+    on(q.device, stream, _fwd, q, k, v, o, lse, mask, mods, scale, causal, code)
 
 
-def _fwd(raw, keep, q, k, v, o, lse, mods, scale, causal, code):
+def _fwd(raw, keep, q, k, v, o, lse, mask, mods, scale, causal, code):
+    if mask is not None:
+        mask.used_on(raw)
     base._raise(base.load_library().fa_fwd_mod(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
                                                *mods, float(scale), int(causal), code, raw), "fa_fwd_mod")
 
@@ -196,7 +207,7 @@ def fa_bwd_mod(q, k, v, o, do, lse, dq, dk, dv, workspace, scale: float, causal:
     base._ws(workspace)
     if workspace.device != q.device:
         raise ValueError(f"workspace must be on {q.device}")
-    on(q.device, stream, _bwd, q, k, v, o, do, lse, dq, dk, dv, workspace, mods, scale, causal, code)
+    on(q.device, stream, _bwd, q, k, v, o, do, lse, dq, dk, dv, workspace, mask, mods, scale, causal, code)
 
 
 def _check_grads(q, o, do, lse, B, H, N, D):
@@ -205,7 +216,9 @@ def _check_grads(q, o, do, lse, B, H, N, D):
     check_on(lse, "lse", torch.float32, (B, H, N), q.device)
 
 
-def _bwd(raw, keep, q, k, v, o, do, lse, dq, dk, dv, workspace, mods, scale, causal, code):
+def _bwd(raw, keep, q, k, v, o, do, lse, dq, dk, dv, workspace, mask, mods, scale, causal, code):
+    if mask is not None:
+        mask.used_on(raw)
     base._raise(base.load_library().fa_bwd_mod(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), do.data_ptr(), lse.data_ptr(), dq.data_ptr(),
         dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), *mods,
@@ -220,7 +233,13 @@ def modified(q, k, mask, softcap, alibi_slopes) -> bool:
 
 
 def _fits(mask, q):
-    return mask is None or (isinstance(mask, AttentionMask) and q.shape[0] == mask.B and q.shape[2] == mask.N)
+    """Whether a call may go to _fast with this mask, which is then kept for the current stream."""
+    if mask is None:
+        return True
+    if not (isinstance(mask, AttentionMask) and q.shape[0] == mask.B and q.shape[2] == mask.N):
+        return False
+    mask.used_on(_raw_stream(mask.plan.device.index))
+    return True
 
 
 def modified_forward(q, k, v, scale, causal, stream, mask, softcap, alibi_slopes):
@@ -233,7 +252,7 @@ def modified_forward(q, k, v, scale, causal, stream, mask, softcap, alibi_slopes
 
     def call(raw, keep):
         o, lse = keep(torch.empty_like(q)), keep(q.new_empty(q.shape[:3], dtype=torch.float32))
-        _fwd(raw, keep, q, k, v, o, lse, mods, scale, causal, code)
+        _fwd(raw, keep, q, k, v, o, lse, mask, mods, scale, causal, code)
         return o, lse
 
     return on(q.device, stream, call)
@@ -257,7 +276,7 @@ def modified_backward(q, k, v, o, lse, do, scale, causal, stream, workspace, mas
         ws = workspace
         if ws is None:
             ws = q.new_empty(base.fa_bwd_workspace_size(B, H, N, D), dtype=torch.uint8)
-        _bwd(raw, keep, q, k, v, o, do, lse, *grads, ws, mods, scale, causal, code)
+        _bwd(raw, keep, q, k, v, o, do, lse, *grads, ws, mask, mods, scale, causal, code)
         return tuple(grads)
 
     return on(q.device, stream, call)

@@ -255,3 +255,31 @@ def test_results_without_the_module_of_the_small_calls(monkeypatch):
     want = step()
     monkeypatch.setattr(base, "_fast", None)
     assert all(torch.equal(a, b) for a, b in zip(step(), want))
+
+
+@pytest.mark.parametrize("how", ["argument", "context"])
+def test_a_mask_may_be_dropped_while_another_stream_reads_it(how):
+    """The plan's memory is not handed out again before the call on the other stream has run."""
+    B, N = 1, 4096
+    q, k, v, do = (rand((B, 1, N, 64), "bf16", s).cuda() for s in range(4))
+    o, lse = fa.attention_forward(q, k, v, mask=fa.attention_mask(B, N, device="cuda", window=100))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda m, s: fa.attention_forward(q, k, v, mask=m, stream=s),
+                 lambda m, s: fa.attention_backward(q, k, v, o, lse, do, mask=m, stream=s)):
+        torch.cuda.empty_cache()
+        mask = fa.attention_mask(B, N, device="cuda", window=100)
+        at, size = mask.plan.data_ptr(), mask.plan.numel()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000_000)                      # a tenth of a second
+            if how == "context":
+                out = call(mask, None)
+        if how == "argument":
+            out = call(mask, side)
+        del mask
+        others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        busy = not side.query()
+        assert busy and at not in [t.data_ptr() for t in others]
+        torch.cuda.synchronize()
+        del out, others
