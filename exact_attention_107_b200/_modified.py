@@ -139,12 +139,12 @@ def attention_mask(B: int, N: int, *, documents=None, prefix=None, causal: bool 
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     if base.fast_path(stream):
-        r = base.fast_result(base._fast.mask_plan(documents, prefix, B, N, causal, window, device.index), "attention_mask")
+        r = base.fast_result(base._fast.mask_plan(documents, prefix, B, N, causal, window, device.index), "fa_mask_plan")
         if r is not None:
             return AttentionMask(r[0], B, N, _raw_stream(device.index))
     size = fa_mask_plan_size(B, N)
     if size == 0:
-        raise base.FAError(2, "attention_mask")
+        raise base.FAError(2, "fa_mask_plan")
     plan, raw = on(device, stream, _new_plan, device, size)
     fa_mask_plan(plan, documents, prefix, B, N, causal, window, stream)
     return AttentionMask(plan, B, N, raw)

@@ -283,3 +283,106 @@ def test_a_mask_may_be_dropped_while_another_stream_reads_it(how):
         assert busy and at not in [t.data_ptr() for t in others]
         torch.cuda.synchronize()
         del out, others
+
+
+def outcome(call):
+    try:
+        r = call()
+    except Exception as e:                                      # noqa: BLE001 - its type and text are compared
+        return type(e), str(e)
+    return [None if t is None else torch.nan_to_num(t.float()).cpu() for t in (r if isinstance(r, tuple) else (r,))]
+
+
+def test_both_host_paths_accept_and_refuse_alike(monkeypatch):
+    """Calls near the edge of what is allowed: the C++ marshalling and the Python path take the same
+    ones, with the same results, and refuse the others with the same error."""
+    B, H, Hkv, N, D, page = 2, 4, 2, 20, 64, 16
+    q, k, v, do = (rand((B, h, N, D), "bf16", s).cuda() for s, h in enumerate((H, Hkv, Hkv, H)))
+    table, pos = fa.rotary_table(N, D).cuda(), torch.arange(N, dtype=torch.int32, device="cuda")
+    slopes = torch.ones(H, device="cuda")
+    kp, vp = (rand((6, Hkv, page, D), "bf16", s).cuda() for s in (5, 6))
+    bt, sl = torch.arange(6, dtype=torch.int32).view(B, 3).cuda(), ints(20, 33).cuda()
+    o, lse = fa.attention_forward(q, k, v, causal=True)
+    ids = torch.zeros(B, N, dtype=torch.int32, device="cuda")
+    mask = fa.attention_mask(B, N, documents=ids)
+    wide = torch.zeros(B, H, N, 80, dtype=torch.bfloat16, device="cuda")
+    param = torch.nn.Parameter(q.clone())
+    cpu = q.cpu()
+    rotary = [dict(), dict(positions=pos), dict(positions=pos[None]), dict(positions=pos.expand(B, N)),
+              dict(positions=pos.repeat(B, 1)), dict(positions=pos[:-1]), dict(positions=pos.long()), dict(positions=pos.cpu()),
+              dict(positions=pos[None, None]), dict(positions=pos.repeat(3, 1)), dict(positions=0), dict(interleaved=1),
+              dict(interleaved=2), dict(interleaved=None), dict(table=table[:, :32].contiguous()), dict(table=table[:, ::2]),
+              dict(table=table[:0]), dict(table=table[0]), dict(table=table.double()), dict(table=None), dict(table=table.cpu()),
+              dict(q=None), dict(k=None), dict(q=None, k=None), dict(q=param), dict(q=cpu), dict(q=q[0]), dict(q=q.float()),
+              dict(q=q.half()), dict(k=k[:1]), dict(k=k[:, :0]), dict(q=q[:, :, :0], k=k[:, :, :0]), dict(k=k[..., :32]),
+              dict(q=wide[..., 8:72]), dict(q=wide[..., 4:68]), dict(q=wide[..., :64].transpose(1, 2)), dict(q=q[:, :1].expand(B, H, N, D)),
+              dict(q=q.flip(2)), dict(q=wide, k=None), dict(q=1)]
+    att = [dict(), dict(causal=True), dict(causal=1), dict(causal=2), dict(causal=None), dict(mask=mask), dict(mask=mask, causal=True),
+           dict(mask=mask.plan), dict(mask=fa.attention_mask(1, N, documents=ids[:1])), dict(softcap=5), dict(softcap=5.0), dict(softcap=True),
+           dict(softcap=-5.0), dict(softcap="5"), dict(scale=1), dict(scale=0.0), dict(scale=float("nan")), dict(scale=10 ** 400),
+           dict(alibi_slopes=slopes), dict(alibi_slopes=slopes[:2]), dict(alibi_slopes=slopes.half()), dict(alibi_slopes=slopes[None]),
+           dict(alibi_slopes=slopes.cpu()), dict(q=param), dict(k=k.half()), dict(k=cpu), dict(v=v[:, :1]), dict(v=v[..., :32]),
+           dict(q=q[:, :3].contiguous()), dict(q=q.transpose(1, 2)), dict(k=k[:, :0], v=v[:, :0]), dict(q=q.float(), k=k.float(), v=v.float()),
+           dict(q=wide, k=wide[:, :2].contiguous(), v=wide[:, :2].contiguous())]
+    back = [dict(), dict(o=o[:1]), dict(lse=lse[:, :1]), dict(lse=lse.half()), dict(do=do.half()), dict(do=do.transpose(1, 2)),
+            dict(do=do[..., :32]), dict(o=o.cpu())]
+    new = k[:, :, :3].contiguous()
+    append = [dict(), dict(new_lens=ints(1, 3).cuda()), dict(new_lens=ints(1, 3)), dict(new_lens=ints(1).cuda()), dict(new_lens=2),
+              dict(q=q[:, :, :3].contiguous()), dict(q=q[:, :, :3]), dict(q=q), dict(q=q[:, :, :3], table=None), dict(table=None),
+              dict(table=table[:, :40]), dict(k=new[:1]), dict(k=k[:, :, :3]), dict(v=new.half()), dict(k_pages=kp[:, :1].contiguous()),
+              dict(k_pages=kp[:, :, :12].contiguous(), v_pages=vp[:, :, :12].contiguous()), dict(k_pages=kp.transpose(1, 2)),
+              dict(v_pages=vp.cpu()), dict(k_pages=kp[:0], v_pages=vp[:0]), dict(block_table=bt[:1]), dict(block_table=bt[:, :0]), dict(block_table=bt.long()),
+              dict(seq_lens=sl[:1]), dict(seq_lens=sl[None]), dict(seq_lens=sl.long()), dict(interleaved=True), dict(interleaved=3),
+              dict(k=new[:, :, :0], v=new[:, :, :0]), dict(k=torch.nn.Parameter(new))]
+    q1 = q[:, :, :2].contiguous()
+    decode = [dict(), dict(softcap=3), dict(softcap=None), dict(scale=None), dict(scale=-1.0), dict(window=3), dict(window=True), dict(window=-1), dict(window=2.0),
+              dict(window=None), dict(alibi_slopes=slopes), dict(alibi_slopes=slopes[:1]), dict(alibi_slopes=slopes.double()), dict(q=q[:, :, :2]),
+              dict(q=q1[:1]), dict(q=q1[0]), dict(q=q1.float()), dict(q=q1.half()), dict(q=q1[:, :3].contiguous()), dict(q=q1[:, :, :0]), dict(q=torch.nn.Parameter(q1)),
+              dict(k_pages=kp[..., :32]), dict(v_pages=vp[:, :1].contiguous()), dict(k_pages=kp[:, :, :12].contiguous(), v_pages=vp[:, :, :12].contiguous()),
+              dict(block_table=bt[0]), dict(block_table=bt[:, :2]), dict(block_table=bt[:, :0].contiguous()), dict(seq_lens=sl[:1]), dict(seq_lens=sl.cpu())]
+    masks = [dict(), dict(documents=ids), dict(documents=ids[:1]), dict(documents=ids.long()), dict(documents=ids.t()), dict(documents=ids.cpu()),
+             dict(prefix=ints(3, 4).cuda()), dict(prefix=ints(3).cuda()), dict(prefix=ints(3, 4).cuda(), causal=False), dict(prefix=ints(3, 4).cuda(), window=2),
+             dict(prefix=ints(3, 4).cuda(), documents=ids), dict(window=3), dict(window=-3), dict(window=2.0), dict(window=True), dict(window=None), dict(causal=0),
+             dict(causal=5), dict(causal=False, window=2), dict(B=0), dict(N=0), dict(N=1 << 19), dict(B=2.0), dict(device="cuda:0"), dict(device="cpu")]
+
+    def rows(plan):
+        n = 2 * B * 128                                          # behind the intervals: unused entries
+        return plan.view(torch.int32)[:n].clone()
+
+    def turned(q=q, k=k, table=table, **kw):
+        return fa.rotary_forward(q, k, table, **kw)
+
+    def attended(q=q, k=k, v=v, scale=None, causal=False, **kw):
+        return fa.attention_forward(q, k, v, scale, causal, **kw)
+
+    def gradients(o=o, lse=lse, do=do):
+        return fa.attention_backward(q, k, v, o, lse, do, causal=True)[1:]
+
+    def appended(k=new, v=new, k_pages=kp, v_pages=vp, block_table=bt, seq_lens=sl, table=table, **kw):
+        out = fa.paged_append(k, v, k_pages, v_pages, block_table, seq_lens, table=table, **kw)
+        return out, k_pages, v_pages
+
+    def decoded(q=q1, k_pages=kp, v_pages=vp, block_table=bt, seq_lens=sl, **kw):
+        return fa.paged_attention(q, k_pages, v_pages, block_table, seq_lens, **kw)
+
+    def planned(B=B, N=N, **kw):
+        return rows(fa.attention_mask(B, N, **{"device": "cuda", **kw}).plan)
+
+    took = 0
+    for f, cases in ((turned, rotary), (attended, att), (gradients, back), (appended, append), (decoded, decode), (planned, masks)):
+        for kw in cases:
+            with monkeypatch.context() as m:
+                pools = kp.clone(), vp.clone()
+                a = outcome(lambda: f(**kw))
+                kp.copy_(pools[0]), vp.copy_(pools[1])
+                m.setattr(base, "_fast", None)
+                b = outcome(lambda: f(**kw))
+                kp.copy_(pools[0]), vp.copy_(pools[1])
+            fa.fa_device_status(reset=True)
+            what = f.__name__, {n: tuple(x.shape) if isinstance(x, torch.Tensor) else x for n, x in kw.items()}
+            if isinstance(a, tuple) or isinstance(b, tuple):
+                assert a == b, (what, a, b)
+            else:
+                took += 1
+                assert len(a) == len(b) and all((x is y) or torch.equal(x, y) for x, y in zip(a, b)), what
+    assert took >= 40
