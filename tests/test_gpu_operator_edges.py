@@ -386,3 +386,57 @@ def test_both_host_paths_accept_and_refuse_alike(monkeypatch):
                 took += 1
                 assert len(a) == len(b) and all((x is y) or torch.equal(x, y) for x, y in zip(a, b)), what
     assert took >= 40
+
+
+@pytest.mark.parametrize("H,Hkv,T,lens,page,cap,window,dtype", [
+    (16, 1, 5, [700, 80], 32, 0.0, 0, "bf16"),                  # 80 rows: three groups
+    (9, 1, 11, [1500, 7, 128], 16, 20.0, 300, "fp16"),           # 99: four, the last of three rows
+    (24, 2, 64, [64, 500], 128, 0.0, 0, "bf16"),                 # 768: the most tokens
+])
+def test_decode_several_groups_of_rows_at_256_columns(H, Hkv, T, lens, page, cap, window, dtype):
+    B, D, wide = len(lens), 256, -(-max(lens) // page)
+    q = rand((B, H, T, D), dtype, 1, 2.0)
+    kp, vp = (rand((B * wide, Hkv, page, D), dtype, s) for s in (2, 3))
+    bt = torch.randperm(B * wide, generator=torch.Generator().manual_seed(4)).int().view(B, wide)
+    want = ref.paged_attention(q, kp, vp, bt, ints(*lens), ref.default_scale(D), cap, None, window)
+    o, l = fa.paged_attention(q.cuda(), kp.cuda(), vp.cuda(), bt.cuda(), ints(*lens).cuda(), softcap=cap, window=window)
+    ref.check(o, want[0], want[2], "O")
+    ref.check(l, want[1], want[3], "lse")
+
+
+@pytest.mark.parametrize("B,H,Hkv,N,D,kind,cap,alibi,dtype", [
+    (1, 3, 1, 450, 128, "causal", 0.0, False, "bf16"), (1, 5, 1, 400, 96, "documents", 0.0, False, "bf16"),
+    (2, 3, 1, 500, 128, "documents", 30.0, False, "fp16"), (1, 6, 2, 450, 128, "full", 0.0, True, "bf16"),
+    (1, 5, 1, 420, 64, "documents", 0.0, True, "fp16"), (1, 9, 3, 390, 96, "causal", 20.0, True, "bf16")])
+def test_odd_groups_walk_all_their_heads(B, H, Hkv, N, D, kind, cap, alibi, dtype):
+    """Groups of 3 and 5 query heads with several query tiles each: one CTA goes from head to head."""
+    q, k, v, do = (rand((B, h, N, D), dtype, s, 1.5) for s, h in enumerate((H, Hkv, Hkv, H)))
+    ids = (torch.arange(N) * 4 // N).int().repeat(B, 1)
+    ids[:, N - 30:] = -1
+    slopes = torch.tensor([0.5 / (h + 1) for h in range(H)]) if alibi else None
+    seen = ref.visible(B, N, documents=ids) if kind == "documents" else ref.visible(B, N, causal=kind == "causal")
+    want, bound = ref.attention(q, k, v, do, 0.09, seen, cap, slopes)
+    d = [t.cuda() for t in (q, k, v, do)]
+    more = dict(mask=fa.attention_mask(B, N, documents=ids.cuda()) if kind == "documents" else None, softcap=cap,
+                alibi_slopes=None if slopes is None else slopes.cuda())
+    o, lse = fa.attention_forward(*d[:3], 0.09, kind == "causal", **more)
+    grads = fa.attention_backward(*d[:3], o, lse, d[3], 0.09, kind == "causal", **more)
+    for name, t in zip(("O", "lse", "dQ", "dK", "dV"), (o, lse, *grads)):
+        ref.check(t, want[name], bound[name], name)
+
+
+@pytest.mark.parametrize("D,causal,cap", [(128, True, 0.0), (96, False, 20.0)])
+def test_many_items_walk_even_groups_in_one_cta(D, causal, cap):
+    """Enough key tiles that pairs of heads are not split over CTAs (four items an SM): two of the
+    key-value heads against the 64-bit form."""
+    B, H, Hkv, N = 5, 64, 32, 400
+    g = torch.Generator(device="cuda").manual_seed(D)
+    q, k, v, do = (torch.randn(B, h, N, D, generator=g, device="cuda").bfloat16() for h in (H, Hkv, Hkv, H))
+    o, lse = fa.attention_forward(q, k, v, causal=causal, softcap=cap)
+    dq, dk, dv = fa.attention_backward(q, k, v, o, lse, do, causal=causal, softcap=cap)
+    for b, h in ((0, 0), (4, 31)):
+        two, one = (slice(b, b + 1), slice(2 * h, 2 * h + 2)), (slice(b, b + 1), slice(h, h + 1))
+        want, bound = ref.attention(*(t[i].cpu() for t, i in ((q, two), (k, one), (v, one), (do, two))), ref.default_scale(D),
+                                    ref.visible(1, N, causal=causal), cap)
+        for name, t, i in (("O", o, two), ("lse", lse, two), ("dQ", dq, two), ("dK", dk, one), ("dV", dv, one)):
+            ref.check(t[i], want[name], bound[name], name)
