@@ -1,4 +1,4 @@
-"""Derives the polynomial used by tanh_poly2() in sm100_ptx.cuh.
+"""Derives the polynomial of tanh behind quartic2(), tanh_any() and quartic_inverse() in sm100_ptx.cuh.
 
 tanh(z) = z g(z^2) with g(u) = tanh(sqrt u) / sqrt u, smooth in u.  The quartic in u that minimises
 the maximum *relative* error of g on [0, LIMIT^2] comes from the Remez exchange algorithm
@@ -6,7 +6,8 @@ the maximum *relative* error of g on [0, LIMIT^2] comes from the Remez exchange 
 
     python exact_attention_107_b200/csrc/gen_tanh_poly.py
 
-prints the coefficients (as float32 hex) and the maximum relative error of the float32 evaluation.
+prints the coefficients and the inverse's chord (as float32 hex), the maximum relative error of the
+float32 evaluation and the inverse's error.
 The kernels only need the printed values; this script documents where they come from and is not
 part of the build.
 """
@@ -53,11 +54,40 @@ def eval_f32(z: np.ndarray, c: np.ndarray) -> np.ndarray:
     return z * p
 
 
+def chord(c: np.ndarray):
+    """Where quartic_inverse starts: the polynomial's value at LIMIT, and the slope of the chord of its
+    inverse from there to 1."""
+    z = np.polynomial.Polynomial(np.stack([np.zeros(len(c)), c.astype(np.float64)], 1).ravel())
+    at = z(LIMIT)
+    one = min(r.real for r in (z - 1.0).roots() if abs(r.imag) < 1e-12 and r.real > LIMIT)
+    return np.float32(at), np.float32((one - LIMIT) / (1.0 - at))
+
+
+def inverse_f32(t: np.ndarray, c: np.ndarray) -> np.ndarray:
+    """quartic_inverse's steps in float32: three Newton steps from the chord."""
+    t, c = t.astype(np.float32), c.astype(np.float32)
+    at, slope = chord(c)
+    z = (t - at) * slope + np.float32(LIMIT)
+    for _ in range(3):
+        u = z * z
+        p, d = np.full_like(z, c[-1]), np.full_like(z, np.float32(2 * TERMS - 1) * c[-1])
+        for j in range(TERMS - 2, -1, -1):
+            p, d = p * u + c[j], d * u + np.float32(2 * j + 1) * c[j]
+        z = z - (z * p - t) / d
+    return z
+
+
 if __name__ == "__main__":
     c = remez_relative()
     c32 = c.astype(np.float32)
     for j, v in enumerate(c32):
         print(f"constexpr float kTanhC{j} = {v:.17f}f;   // 0x{v.tobytes()[::-1].hex()}")
+    for name, v in zip(("kTanhAtLimit", "kTanhChord"), chord(c32)):
+        print(f"constexpr float {name} = {v:.17f}f;   // 0x{v.tobytes()[::-1].hex()}")
     z = np.linspace(1e-6, LIMIT, 1_000_001).astype(np.float32)
     rel = np.abs(eval_f32(z, c32).astype(np.float64) / np.tanh(z.astype(np.float64)) - 1.0)
     print(f"max relative error over (0, {LIMIT}]: {rel.max():.3e}")
+    t = np.linspace(float(chord(c32)[0]), 1.0, 1_000_001).astype(np.float32)
+    back = inverse_f32(t, c32).astype(np.float64)
+    value = back * np.polynomial.polynomial.polyval(back * back, c32.astype(np.float64))
+    print(f"max error of the polynomial at its inverse: {np.abs(value - t).max():.3e}")

@@ -394,10 +394,13 @@ __device__ __forceinline__ float2 quartic2(float2 x, const float (&c)[5]) {
   p = __ffma2_rn(p, u, make_float2(c[1], c[1]));
   return __ffma2_rn(p, u, make_float2(c[0], c[0]));
 }
-// tanh's quartic beyond its limit: z' with z' (C0 + C1 z'^2 + ...) = t for kTanhPolyLimit's tanh
-// <= t <= 1 (the polynomial rises to 1 at z' = 1.477).  Three Newton steps from a chord leave 2^-22.
+// tanh's quartic beyond its limit: z' with z' (C0 + C1 z'^2 + ...) = t for kTanhAtLimit (the quartic's
+// value at the limit) <= t <= 1 (it rises to 1 at z' = 1.477).  Three Newton steps from the chord of
+// the inverse between the two leave 2^-22 (gen_tanh_poly.py derives the chord and checks the steps).
+constexpr float kTanhAtLimit = 0.63514935970306396f;   // 0x3f229926
+constexpr float kTanhChord = 1.99241662025451660f;     // 0x3fff0782
 __device__ __forceinline__ float quartic_inverse(float t) {
-  float z = fmaf(t - 0.63514936f, 1.9726f, kTanhPolyLimit);
+  float z = fmaf(t - kTanhAtLimit, kTanhChord, kTanhPolyLimit);
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     const float u = z * z;

@@ -1,11 +1,14 @@
 """Edges of the rotary, paged-cache and score-modified operators without a GPU: index arithmetic at
 the ends of its range, arguments beyond C's types, and the package without one of its parts."""
 import ctypes
+import importlib.util
+import re
 import shutil
 import subprocess
 import sys
 from pathlib import Path
 
+import numpy as np
 import pytest
 
 import exact_attention_107_b200 as fa
@@ -144,3 +147,19 @@ except ValueError as e:
 else:
     raise SystemExit("not refused")
 """)
+
+
+def test_inverse_of_the_tanh_polynomial():
+    """The header's chord is the generator's, and the steps from it leave 2^-22."""
+    spec = importlib.util.spec_from_file_location("gen_tanh_poly", CSRC / "gen_tanh_poly.py")
+    g = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(g)
+    c = g.remez_relative().astype(np.float32)
+    text = (CSRC / "sm100_ptx.cuh").read_text()
+    for name, want in zip(("kTanhAtLimit", "kTanhChord"), g.chord(c)):
+        value, word = re.search(rf"{name} = ([0-9.]+)f;\s*// 0x([0-9a-f]{{8}})", text).groups()
+        assert np.float32(value) == want and np.frombuffer(bytes.fromhex(word)[::-1], np.float32)[0] == want
+    t = np.linspace(float(g.chord(c)[0]), 1.0, 300001).astype(np.float32)
+    z = g.inverse_f32(t, c).astype(np.float64)
+    p = z * np.polynomial.polynomial.polyval(z * z, c.astype(np.float64))
+    assert np.abs(p - t).max() <= 2.0 ** -22 and (np.diff(z) >= -2.0 ** -21).all() and z[0] >= g.LIMIT - 2.0 ** -21
