@@ -153,9 +153,12 @@ struct NoLock {
 // (torch.OutOfMemoryError for an allocation that fails).
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* guard(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  HANDLE_TH_ERRORS
-  return F(a, n);
-  END_HANDLE_TH_ERRORS
+  try {
+    return F(a, n);
+  } catch (...) {
+    torch::translate_exception_to_python(std::current_exception());
+    return nullptr;
+  }
 }
 
 // (q | None, k | None, table, positions | None, interleaved, inverse) -> (q, k)
