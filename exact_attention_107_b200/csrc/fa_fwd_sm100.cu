@@ -86,8 +86,10 @@ struct FwdSmem {
 //          the softmax runs on cap log2e tanh.  Two MUFU operations a score for an accurate tanh
 //          next to the exponential's one made the MUFU unit the limit (B1 H8 N16384 D128 causal:
 //          1176 us against 483 without a cap); scores up to 0.75 cap, as nearly all are, take a
-//          polynomial on the FMA pipe instead (a warp's choice for its 32 rows of a tile): 695 us.
-//   ALIBI  x -= slope_h |i - j|, in fp32, joined to the exponent (642 us).
+//          polynomial on the FMA pipe instead (a warp's choice for its 32 rows of a tile).
+//   ALIBI  x -= slope_h |i - j|, in fp32, joined to the exponent.
+// At that size 469 us plain, 647 capped, 638 with a bias, 875 with both.  The capped instances spill
+// 28 bytes of the 168 registers a thread, those with a bias too 80 to 84.
 // Rows that see nothing get O = 0 and lse = -inf.
 template <int D, bool CAUSAL, bool F16, bool MOD, bool CAP, bool ALIBI>
 __global__ void __launch_bounds__(kThreads, 1)

@@ -11,10 +11,11 @@
 // and a row's maximum is a warp reduction and four values in shared memory.
 //
 // Bound by memory: K and V of the visible positions are read once, 4 D bytes a position and head,
-// against 4 M D operations.  So the loads never pause: one warp looks up pages (each lane one page
-// of the tile, the next tile's while this one waits for room) and issues one TMA box per page and
-// 64 columns into a ring of tile slots of 128 to 192 KB a CTA; the 128-byte swizzle makes the boxes
-// of a tile's pages one operand tile.  The MMA warp runs one tile of S^T ahead of the softmax.
+// against 4 M D operations.  So the loads never pause: K and V have a warp each, which looks up pages
+// (each lane one page of the tile, the next tile's while this one waits for room) and issues one TMA
+// box per page and 64 columns into its own ring of tile slots, 128 to 192 KB a CTA for both; the
+// 128-byte swizzle makes the boxes of a tile's pages one operand tile.  The MMA warp runs one tile of
+// S^T ahead of the softmax.
 //
 // The work is split over the caches' length, evenly and whatever their lengths: all units' tiles
 // form one line, sequence after sequence, and each of the CTAs (one per SM) takes an equal piece of
@@ -25,9 +26,11 @@
 //
 // Measured (one B200, whole call): 48 sequences of up to 8192, 32 heads on 8, D = 128, pages of 16:
 // 162 us, 5.5 TB/s; one sequence of 262144, 16 heads on 2: 52 us, 5.1 TB/s; 17 sequences of up to
-// 6000, 5 new tokens, D = 256, window 4096: 54 us, 4.4 TB/s; one sequence of 500: 9.5 us.  Not bound
-// by memory where a tile is small (D = 64: 3.9 TB/s at 16 sequences of 4096 and 32 heads; there the
-// thread that issues both products is busy throughout) or R is 64 (2.4 TB/s: the exponentials).  Two
+// 6000, 5 new tokens, D = 256, window 4096: 55 us, 4.3 TB/s; one sequence of 500: 9.5 us.  Not bound
+// by memory where a tile is small (16 sequences of 4096, 32 heads: D = 64 146 us, 3.7 TB/s, and D = 32
+// as long; there the thread that issues both products is busy throughout) or R is 64 (16 sequences of
+// 8192, 8 key-value heads of D = 128: 122 us with 16 rows, 130 with 32, 185 or 2.9 TB/s with 64: the
+// exponentials, of 64 rows in 255 registers with 48 to 64 bytes spilled).  Two
 // softmax warpgroups with a piece each, and a warp for either product, were built and measured: a few
 // percent faster at D <= 64, up to a third slower at R = 32 and D = 256 (168 registers a thread).
 //

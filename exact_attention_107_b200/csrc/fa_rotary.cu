@@ -16,7 +16,9 @@
 // Measured: 8 x 4096 tokens of 16 + 4 heads, D = 128, half layout 57 us (5.9 TB/s); 32767 tokens of
 // 8 + 8 heads, interleaved, R = 64: 51 us (5.4 TB/s); append of 5 x 2000 ragged rows 22.8 us.  Half
 // layouts with R not a multiple of 16 are bound by their shared-memory reads of single values: R = 66
-// takes twice R = 128's time.
+// takes twice R = 128's time.  The launch bound of four blocks an SM holds threads to 64 registers:
+// the append's ordinary half layout spills 32 bytes there and is faster than with three blocks all
+// the same (launch_layout), the odd half layouts spill 36 to 48.
 #include <cstdint>
 
 #include "fa_internal.h"

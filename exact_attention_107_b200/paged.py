@@ -155,7 +155,8 @@ def paged_attention(q, k_pages, v_pages, block_table, seq_lens, scale: float | N
     q (B,H,T,D), H a multiple of the pages' Hkv.  Row t of sequence b has position p =
     seq_lens[b] - T + t and sees keys j <= p, with window > 0 those with p - j < window; a row with
     p < 0 has O = 0 and lse = -inf.  softcap and alibi_slopes as in attention_forward, so that a
-    model trained there is served here.  Table entries past a sequence's last page, or wholly before
+    model trained there (head dims up to 128 with these) is served here; this call takes 256 columns
+    too.  Table entries past a sequence's last page, or wholly before
     every row's window, are not read; a page outside the pool counts as absent and sets the device
     status (fa_device_status) to FA_ERR_INDEX.  workspace: for callers that keep one, of
     fa_paged_workspace_size bytes; calls that may overlap on the GPU (other streams, captured

@@ -184,7 +184,8 @@ def _readable(t):
 
 
 class RotaryEmbedding(torch.autograd.Function):
-    """autograd wrapper of rotary_forward / rotary_backward."""
+    """autograd wrapper of rotary_forward / rotary_backward.  Under CUDA graph capture the rule of
+    ModifiedAttention holds."""
 
     @staticmethod
     def forward(ctx, q, k, table, positions, interleaved):
