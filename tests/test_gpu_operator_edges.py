@@ -272,7 +272,7 @@ def test_a_mask_may_be_dropped_while_another_stream_reads_it(how):
         at, size = mask.plan.data_ptr(), mask.plan.numel()
         side.wait_stream(torch.cuda.current_stream())
         with torch.cuda.stream(side):
-            torch.cuda._sleep(200_000_000)                      # a tenth of a second
+            torch.cuda._sleep(1_000_000_000)                    # half a second
             if how == "context":
                 out = call(mask, None)
         if how == "argument":
